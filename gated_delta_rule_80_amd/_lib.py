@@ -140,6 +140,8 @@ def load(path: str | None = None) -> ctypes.CDLL:
     lib.kda_prefill_forward_saved.argtypes = [P(PrefillArgs), _vp, ctypes.c_size_t, _vp]
     lib.kda_prefill_backward_saved.restype = ctypes.c_int
     lib.kda_prefill_backward_saved.argtypes = [P(BackwardArgs), _vp, ctypes.c_size_t, _vp]
+    from . import _gdr
+    _gdr.declare(lib)
     if lib.kda_abi_version() != ABI_VERSION:
         raise RuntimeError("libkda ABI version mismatch")
     if path is None:

@@ -23,7 +23,9 @@ BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libkda.so")
 
 SOURCES = ["kda_api.cpp", "kda_noalloc.hip", "kda_prep.hip", "kda_prep_exact.hip", "kda_state.hip",
-           "kda_decode.hip", "kda_backward.hip", "kda_bwd_stages.hip", "kda_split.hip"]
+           "kda_decode.hip", "kda_backward.hip", "kda_bwd_stages.hip", "kda_split.hip",
+           "kda_gdr_api.cpp", "kda_gdr_prep.hip", "kda_gdr_walk.hip",
+           "kda_gdr_reverse.hip", "kda_gdr_grad.hip", "kda_gdr_decode.hip", "kda_pages.hip"]
 ARCH = "gfx950"
 
 

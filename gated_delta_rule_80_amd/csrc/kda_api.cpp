@@ -9,44 +9,24 @@
 #include <initializer_list>
 #include <utility>
 
+#include "kda_host.h"
 #include "kda_launch.h"
 #include "kda_layout.h"
 
 namespace {
 
+using kda::aligned16;
+using kda::esize;
+using kda::hip_status;
+using kda::mul_ok;
+using kda::overlaps;
 using kda::record_layout;
+using kda::same_or_disjoint;
+using kda::Span;
+using kda::span;
 
-struct Span {
-  uintptr_t lo = 0, hi = 0;  // [lo, hi); empty when lo == hi
-};
-
-Span span(const void* p, size_t bytes) {
-  Span s;
-  if (p != nullptr && bytes > 0) {
-    s.lo = reinterpret_cast<uintptr_t>(p);
-    s.hi = s.lo + bytes;
-  }
-  return s;
-}
-bool overlaps(Span a, Span b) { return a.lo < a.hi && b.lo < b.hi && a.lo < b.hi && b.lo < a.hi; }
-bool same_or_disjoint(Span a, Span b) { return (a.lo == b.lo && a.hi == b.hi) || !overlaps(a, b); }
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 bool supported_d(int D) { return D == 16 || D == 32 || D == 64 || D == 128; }
 bool supported_chunk(int C) { return C == 16 || C == 32 || C == 64; }
-size_t esize(int io) { return io == KDA_FP32 ? 4 : 2; }
-
-// a * b * c * d without overflow past 2^62; returns false on overflow.
-bool mul_ok(size_t& out, std::initializer_list<size_t> xs) {
-  size_t acc = 1;
-  for (size_t x : xs) {
-    if (x != 0 && acc > (size_t(1) << 62) / x) return false;
-    acc *= x;
-  }
-  out = acc;
-  return true;
-}
-
-kda_status hip_status(hipError_t e) { return e == hipSuccess ? KDA_OK : KDA_ERR_HIP; }
 
 struct PrefillSizes {
   size_t x;      // bytes of one [B][T][H][D] tensor

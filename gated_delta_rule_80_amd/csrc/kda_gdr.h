@@ -1,0 +1,174 @@
+// The gated delta rule with one decay per head: workspace layout and parameter
+// blocks shared by the host runtime (plain C++) and the kernels.
+//
+// Per value head (query/key head = value head / (Hv / Hk)) and chunk of C tokens,
+// with G_i the cumulative log-decay inside the chunk, gamma_i = e^{G_i},
+// lambda_i = e^{G_C - G_i}, D_ij = e^{G_i - G_j} (j <= i; every exponent <= 0, so
+// no factoring is needed as it is for a decay per channel), k^, q^ the
+// normalised rows (or the rows as given) and b = beta:
+//   a_ij = D_ij (k^_i . k^_j) b_j   (j < i)        Tm = (I + a)^-1
+//   p_ij = scale D_ij (q^_i . k^_j) b_j  (j <= i)
+//   Y = Tm (V - gamma K^ S)         the part of each v that S does not hold yet
+//   O = scale gamma Q^ S + p Y      S' = gamma_C S + (b lambda K^)^T Y
+// Every scale is one number per token, so it multiplies accumulator rows and the
+// matrix operands stay the raw q, k, v of the caller.
+#pragma once
+#include <stddef.h>
+#include <stdint.h>
+
+#include "kda_layout.h"
+
+namespace kda {
+
+// Tokens per chunk: the deepest whose two images of q, k, v and of the chunk's
+// matrices fit LDS together (bf16 64, float32 32).
+constexpr int gdr_chunk(bool fp32) { return fp32 ? 32 : 64; }
+
+// One record per (sequence, value head, chunk), element type E:
+//   Tm   [TT][C][C]  row-major, TT terms: bf16 keeps Tm as hi + lo (16 bits of
+//                    mantissa), float32 as it is
+//   P    [PT][C][C]  row-major: one term for the forward, hi + lo (bf16) for the
+//                    backward, whose dS0 leaves in float32
+//   sc   [8][C]      float32, per token: cx = gamma rk, cy = b lambda rk,
+//                    co = scale gamma rq, rk, rq, G (high part), G (low part),
+//                    b; rows behind the sequence's end hold zeros in cx, cy, co,
+//                    rk, rq, b
+// where rk, rq are 1 / norm (1 without the normalisation).
+struct GdrRecord {
+  size_t t, p, sc;  // byte offsets
+  size_t bytes;     // 256-byte multiple
+};
+constexpr int kGdrScalars = 8;
+
+constexpr GdrRecord gdr_record(bool fp32, bool bwd) {
+  const size_t C = (size_t)gdr_chunk(fp32), es = fp32 ? 4 : 2;
+  const size_t tt = fp32 ? 1 : 2, pt = fp32 ? 1 : (bwd ? 2 : 1);
+  GdrRecord r{};
+  r.t = 0;
+  r.p = tt * C * C * es;
+  r.sc = r.p + pt * C * C * es;
+  r.bytes = round_up(r.sc + kGdrScalars * C * 4, 256);
+  return r;
+}
+
+// Where the rows of a call stand: B equal-length sequences, or packed ones with
+// their tables in the workspace.  Records are chunk-major (rec_slot).
+struct GdrShape {
+  int B, T, Hk, Hv;  // B: rows of tokens (packed: 1)
+  int NS;            // sequences
+  int NT;            // chunk slots per (sequence, head); packed: per head
+  long qs, ks, vs;   // elements between tokens of q, k, v
+  SeqTables seqs;    // bounds NULL: equal lengths
+};
+
+struct GdrPrepParams {
+  GdrShape s;
+  const void* q;
+  const void* k;
+  const void* g;
+  const void* beta;
+  const float* A_log;
+  const float* dt_bias;
+  int beta_logits, l2;
+  float eps, scale;
+  char* rec;
+};
+
+struct GdrWalkParams {
+  GdrShape s;
+  const void* q;
+  const void* k;
+  const void* v;
+  const char* rec;
+  const float* S0;  // NULL: zeros; may equal S_T
+  float* S_T;       // NULL: not written
+  void* o;          // NULL: no output
+  // for the backward: Y [B][T][Hv][Dv] and the state at each chunk's start,
+  // [record][Dv / 16][Dk][16], both in the element type; NULL otherwise
+  void* y;
+  void* ckpt;
+};
+
+struct GdrReverseParams {
+  GdrShape s;
+  const void* q;
+  const void* k;
+  const char* rec;
+  const void* dO;     // [B][T][Hv][Dv]
+  const float* dS_T;  // NULL: zeros
+  float* dS0;         // NULL: not written
+  void* dv;           // [B][T][Hv][Dv]
+  void* ckpt;         // the gradient of each chunk's end state, layout as above
+};
+
+struct GdrGradParams {
+  GdrShape s;
+  const void* q;
+  const void* k;
+  const char* rec;
+  const void* dO;
+  const void* dv;
+  const void* y;
+  const void* ckS;
+  const void* ckdS;
+  void* dq;
+  void* dk;
+  void* dg;        // io type
+  void* dbeta;     // io type
+  float* dg32;     // [B][T][Hv] gradient of the decay in float32, with raw projections
+  int l2;
+  float scale;
+  const void* g;      // raw projections, with A_log
+  const float* A_log;
+  const float* dt_bias;
+  int beta_logits;
+};
+
+struct GdrGateParams {  // sums over the tokens of one head each
+  const void* g;
+  const float* A_log;
+  const float* dt_bias;
+  const float* dg32;   // gradient of the decay
+  float* dA_log;       // or NULL
+  float* ddt_bias;     // or NULL
+  long tokens;
+  int Hv;
+  SeqTables seqs;      // packed: only tokens [bounds[0], bounds[n_seqs]) count
+};
+
+struct GdrDecodeParams {
+  const void* q;
+  const void* k;
+  const void* v;
+  const void* g;
+  const void* beta;
+  const float* A_log;
+  const float* dt_bias;
+  int beta_logits, l2;
+  float eps, scale;
+  float* S;
+  const int* slots;  // NULL: row i uses slot i
+  void* o;
+  int N, n_slots, Hk, Hv;
+  long qs, ks, vs;   // elements between rows
+};
+
+// ------------------------------------------------------------------ pages
+struct PagesMoveParams {
+  const char* src;
+  char* dst;
+  size_t src_layer, dst_layer;  // bytes between layers
+  size_t page_bytes;
+  int layers;
+  const int* moves;
+  const int* count;
+  int cap;                      // most moves there can be
+  // table entries to rename after a compaction (NULL: none)
+  const int* table;
+  int* table_out;
+  const int* new_id;
+  long n_table;
+  int n_pages;
+};
+
+}  // namespace kda

@@ -3,6 +3,7 @@
 #include <hip/hip_runtime.h>
 
 #include "kda.h"
+#include "kda_gdr.h"
 #include "kda_layout.h"
 
 namespace kda {
@@ -39,6 +40,24 @@ hipError_t launch_bwd_empty_history(float* dconv_state, const int* bounds, int n
 int bwd_out_groups(long rows, int D);   // workgroups (= partials) of the two
 int bwd_act_groups(long tokens, int D);
 hipError_t launch_decode(const DecodeParams& p, int D, bool fp32, hipStream_t st);
+
+// the gated delta rule with one decay per head (kda_gdr.h)
+hipError_t launch_gdr_prep(const GdrPrepParams& p, int Dk, bool fp32, bool bwd, hipStream_t st);
+hipError_t launch_gdr_walk(const GdrWalkParams& p, int Dk, int Dv, bool fp32, hipStream_t st);
+hipError_t launch_gdr_reverse(const GdrReverseParams& p, int Dk, int Dv, bool fp32, hipStream_t st);
+hipError_t launch_gdr_grad(const GdrGradParams& p, int Dk, int Dv, bool fp32, hipStream_t st);
+hipError_t launch_gdr_gate(const GdrGateParams& p, bool fp32, hipStream_t st);
+hipError_t launch_gdr_decode(const GdrDecodeParams& p, int Dk, int Dv, bool fp32, hipStream_t st);
+
+// pages of a cache: a plan of one workgroup, then the moves
+hipError_t launch_pages_fork(const int* refs, int* refs_out, int n_pages, const int* src, int* dst, int n,
+                             int* free_list, const PagesMoveParams& m, hipStream_t st);
+hipError_t launch_pages_free(const int* refs, int* refs_out, int n_pages, const int* pages, int n,
+                             hipStream_t st);
+hipError_t launch_pages_compact(const int* refs, int* refs_out, int n_pages, int* new_id, int* n_used,
+                                const PagesMoveParams& m, hipStream_t st);
+hipError_t launch_pages_copy(const int* src, const int* dst, int n, int src_pages, int dst_pages, int same,
+                             int* first, int* done, const PagesMoveParams& m, hipStream_t st);
 
 // The whole prefill (arguments already validated) in a workspace of `bytes`:
 // time slices when the whole-sequence workspace does not fit (B equal-length

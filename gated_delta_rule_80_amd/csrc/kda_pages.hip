@@ -1,0 +1,258 @@
+// Pages of a cache: a pool holds n_pages pages of page_bytes in each of its
+// layers; refs counts the holders of a page (0: free).  A small kernel of one
+// workgroup reads the counts and the request and writes the list of page moves
+// (and the new counts); one grid then moves the bytes.  The lists are built so
+// that no page is both read and written: a fork reads pages in use and writes free
+// ones, a compaction reads pages behind the first n_used and writes free ones
+// before them, a copy leaves such pairs out.
+#include "kda_gdr.h"
+#include "kda_launch.h"
+
+namespace kda {
+
+namespace {
+
+constexpr int PT = 1024;
+typedef unsigned u32x4 __attribute__((ext_vector_type(4)));
+
+// Exclusive running sum over the workgroup's PT threads; *total gets the sum.
+__device__ __forceinline__ int block_excl(int x, int* red, int* total) {
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  int incl = x;
+#pragma unroll
+  for (int m = 1; m < 64; m <<= 1) {
+    const int y = __shfl_up(incl, m, 64);
+    if (lane >= m) incl += y;
+  }
+  if (lane == 63) red[wave] = incl;
+  __syncthreads();
+  int base = 0, sum = 0;
+#pragma unroll
+  for (int w = 0; w < PT / 64; ++w) {
+    if (w < wave) base += red[w];
+    sum += red[w];
+  }
+  __syncthreads();
+  *total = sum;
+  return base + incl - x;
+}
+
+// The k-th valid request takes the k-th free page.  refs_out may be refs.
+__global__ __launch_bounds__(PT) void kda_pages_fork_plan_kernel(const int* refs, int* refs_out, int n_pages,
+                                                                 const int* src, int* dst, int n,
+                                                                 int* moves, int* count, int* free_list) {
+  __shared__ int red[PT / 64];
+  const int tid = threadIdx.x;
+  int nfree = 0, total;
+  for (int base = 0; base < n_pages; base += PT) {
+    const int i = base + tid;
+    const int ref = i < n_pages ? refs[i] : 1;
+    const int k = nfree + block_excl(ref <= 0 ? 1 : 0, red, &total);
+    if (ref <= 0 && k < n) free_list[k] = i;
+    nfree += total;
+  }
+  __syncthreads();
+  int taken = 0;
+  for (int base = 0; base < n; base += PT) {
+    const int i = base + tid;
+    const int s = i < n ? src[i] : -2;
+    const bool ok = s == -1 || (s >= 0 && s < n_pages && refs[s] > 0);
+    const int k = taken + block_excl(ok ? 1 : 0, red, &total);
+    if (i < n) {
+      const int d = ok && k < nfree ? free_list[k] : -1;
+      dst[i] = d;
+      if (d >= 0) {
+        moves[2 * k] = s;
+        moves[2 * k + 1] = d;
+      }
+    }
+    taken += total;
+  }
+  taken = taken < nfree ? taken : nfree;
+  if (tid == 0) *count = taken;
+  __syncthreads();  // every read of refs is done: refs_out may be the same array
+  if (refs_out != refs)
+    for (int i = tid; i < n_pages; i += PT) refs_out[i] = refs[i];
+  __syncthreads();
+  for (int k = tid; k < taken; k += PT) refs_out[free_list[k]] = 1;
+}
+
+// A page's count goes down once for every time it is listed, not below 0.
+__global__ __launch_bounds__(PT) void kda_pages_free_kernel(const int* refs, int* refs_out, int n_pages,
+                                                            const int* pages, int n) {
+  const int tid = threadIdx.x;
+  if (refs_out != refs)
+    for (int i = tid; i < n_pages; i += PT) refs_out[i] = refs[i];
+  __syncthreads();
+  for (int i = tid; i < n; i += PT) {
+    const int pg = pages[i];
+    if (pg < 0 || pg >= n_pages) continue;
+    int have = __hip_atomic_load(refs_out + pg, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_WORKGROUP);
+    while (have > 0 && !__hip_atomic_compare_exchange_strong(refs_out + pg, &have, have - 1,
+                                                             __ATOMIC_RELAXED, __ATOMIC_RELAXED,
+                                                             __HIP_MEMORY_SCOPE_WORKGROUP)) {
+    }
+  }
+}
+
+// Used pages at or behind n_used move to the free pages before it, in order.
+// refs_out may be refs.
+__global__ __launch_bounds__(PT) void kda_pages_compact_plan_kernel(const int* refs, int* refs_out,
+                                                                    int n_pages, int* new_id, int* n_used,
+                                                                    int* moves, int* count) {
+  __shared__ int red[PT / 64];
+  const int tid = threadIdx.x;
+  int used = 0, total;
+  for (int base = 0; base < n_pages; base += PT) {
+    const int i = base + tid;
+    block_excl(i < n_pages && refs[i] > 0 ? 1 : 0, red, &total);
+    used += total;
+  }
+  int nm = 0, nh = 0;
+  for (int base = 0; base < n_pages; base += PT) {
+    const int i = base + tid;
+    const bool held = i < n_pages && refs[i] > 0;
+    const bool mover = held && i >= used, hole = i < n_pages && !held && i < used;
+    const int km = nm + block_excl(mover ? 1 : 0, red, &total);
+    nm += total;
+    const int kh = nh + block_excl(hole ? 1 : 0, red, &total);
+    nh += total;
+    if (mover) moves[2 * km] = i;
+    if (hole) moves[2 * kh + 1] = i;
+    if (i < n_pages) new_id[i] = held ? i : -1;
+  }
+  if (tid == 0) {
+    *count = nm;  // as many holes as movers
+    *n_used = used;
+  }
+  __syncthreads();
+  for (int k = tid; k < nm; k += PT) new_id[moves[2 * k]] = moves[2 * k + 1];
+  // a mover's count goes to its new place; the two sets of places are disjoint
+  for (int k = tid; k < nm; k += PT) refs_out[moves[2 * k + 1]] = refs[moves[2 * k]];
+  __syncthreads();
+  if (refs_out != refs)
+    for (int i = tid; i < used; i += PT)
+      if (refs[i] > 0) refs_out[i] = refs[i];
+  for (int i = used + tid; i < n_pages; i += PT) refs_out[i] = 0;
+}
+
+// Pairs of a copy: of the pairs inside both pools that share a destination the
+// first counts, and none whose source some pair writes (same: one pool).
+__global__ __launch_bounds__(PT) void kda_pages_copy_plan_kernel(const int* src, const int* dst, int n,
+                                                                 int src_pages, int dst_pages, int same,
+                                                                 int* first, int* done, int* moves,
+                                                                 int* count) {
+  __shared__ int red[PT / 64];
+  const int tid = threadIdx.x;
+  for (int i = tid; i < dst_pages; i += PT) first[i] = 0x7fffffff;
+  __syncthreads();
+  for (int i = tid; i < n; i += PT) {
+    const int s = src[i], d = dst[i];
+    if (s >= -1 && s < src_pages && d >= 0 && d < dst_pages) 
+      __hip_atomic_fetch_min(first + d, i, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_WORKGROUP);
+  }
+  __syncthreads();
+  int total, taken = 0;
+  for (int base = 0; base < n; base += PT) {
+    const int i = base + tid;
+    bool ok = false;
+    int s = 0, d = 0;
+    if (i < n) {
+      s = src[i];
+      d = dst[i];
+      ok = s >= -1 && s < src_pages && d >= 0 && d < dst_pages &&
+           __hip_atomic_load(first + d, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_WORKGROUP) == i;
+      if (ok && same && s >= 0)
+        ok = __hip_atomic_load(first + s, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_WORKGROUP) == 0x7fffffff;
+    }
+    const int k = taken + block_excl(ok ? 1 : 0, red, &total);
+    if (ok) {
+      moves[2 * k] = s;
+      moves[2 * k + 1] = d;
+    }
+    if (i < n && done != nullptr) done[i] = ok ? 1 : 0;
+    taken += total;
+  }
+  if (tid == 0) *count = taken;
+}
+
+// One workgroup moves pieces of kPiece bytes: 256 threads x 4 x 16 bytes.
+constexpr int kPiece = 16384;
+
+__global__ __launch_bounds__(256) void kda_pages_move_kernel(PagesMoveParams p) {
+  int count = *p.count;
+  count = count < p.cap ? count : p.cap;
+  const size_t pieces = (p.page_bytes + kPiece - 1) / kPiece;
+  const size_t items = (size_t)count * p.layers * pieces;
+  for (size_t it = blockIdx.x; it < items; it += gridDim.x) {
+    const size_t piece = it % pieces, rest = it / pieces;
+    const int layer = (int)(rest % p.layers), m = (int)(rest / p.layers);
+    const int s = p.moves[2 * m], d = p.moves[2 * m + 1];
+    const size_t off = piece * kPiece;
+    const size_t left = (p.page_bytes - off) / 16;
+    u32x4* to = reinterpret_cast<u32x4*>(p.dst + layer * p.dst_layer + d * p.page_bytes + off);
+    const u32x4* from = reinterpret_cast<const u32x4*>(p.src + layer * p.src_layer +
+                                                       (s < 0 ? 0 : s) * p.page_bytes + off);
+    u32x4 x[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const size_t i = threadIdx.x + 256 * k;
+      x[k] = u32x4{0u, 0u, 0u, 0u};
+      if (s >= 0 && i < left) x[k] = __builtin_nontemporal_load(from + i);
+    }
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const size_t i = threadIdx.x + 256 * k;
+      if (i < left) __builtin_nontemporal_store(x[k], to + i);
+    }
+  }
+  for (long i = (long)blockIdx.x * 256 + threadIdx.x; i < p.n_table; i += (long)gridDim.x * 256) {
+    const int t = p.table[i];
+    p.table_out[i] = t >= 0 && t < p.n_pages ? p.new_id[t] : -1;
+  }
+}
+
+hipError_t move(const PagesMoveParams& m, hipStream_t st) {
+  const size_t pieces = (m.page_bytes + kPiece - 1) / kPiece;
+  size_t grid = (size_t)m.cap * m.layers * pieces;
+  const size_t tab = (size_t)(m.n_table + 255) / 256;
+  if (grid < tab) grid = tab;
+  if (grid == 0) return hipSuccess;
+  if (grid > 4096) grid = 4096;
+  hipLaunchKernelGGL(kda_pages_move_kernel, dim3((unsigned)grid), dim3(256), 0, st, m);
+  return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_pages_fork(const int* refs, int* refs_out, int n_pages, const int* src, int* dst, int n,
+                             int* free_list, const PagesMoveParams& m, hipStream_t st) {
+  hipLaunchKernelGGL(kda_pages_fork_plan_kernel, dim3(1), dim3(PT), 0, st, refs, refs_out, n_pages, src, dst,
+                     n, const_cast<int*>(m.moves), const_cast<int*>(m.count), free_list);
+  if (hipError_t e = hipGetLastError(); e != hipSuccess) return e;
+  return move(m, st);
+}
+
+hipError_t launch_pages_free(const int* refs, int* refs_out, int n_pages, const int* pages, int n,
+                             hipStream_t st) {
+  hipLaunchKernelGGL(kda_pages_free_kernel, dim3(1), dim3(PT), 0, st, refs, refs_out, n_pages, pages, n);
+  return hipGetLastError();
+}
+
+hipError_t launch_pages_compact(const int* refs, int* refs_out, int n_pages, int* new_id, int* n_used,
+                                const PagesMoveParams& m, hipStream_t st) {
+  hipLaunchKernelGGL(kda_pages_compact_plan_kernel, dim3(1), dim3(PT), 0, st, refs, refs_out, n_pages, new_id,
+                     n_used, const_cast<int*>(m.moves), const_cast<int*>(m.count));
+  if (hipError_t e = hipGetLastError(); e != hipSuccess) return e;
+  return move(m, st);
+}
+
+hipError_t launch_pages_copy(const int* src, const int* dst, int n, int src_pages, int dst_pages, int same,
+                             int* first, int* done, const PagesMoveParams& m, hipStream_t st) {
+  hipLaunchKernelGGL(kda_pages_copy_plan_kernel, dim3(1), dim3(PT), 0, st, src, dst, n, src_pages, dst_pages,
+                     same, first, done, const_cast<int*>(m.moves), const_cast<int*>(m.count));
+  if (hipError_t e = hipGetLastError(); e != hipSuccess) return e;
+  return move(m, st);
+}
+
+}  // namespace kda

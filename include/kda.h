@@ -371,6 +371,167 @@ kda_status kda_prefill_forward_saved(const kda_prefill_args* f, void* ws, size_t
 kda_status kda_prefill_backward_saved(const kda_backward_args* a, void* ws, size_t ws_bytes,
                                       void* stream);
 
+/* ------------------------------------- gated delta rule, one decay per head */
+/* The delta rule with ONE log-decay per token and head, whose value heads may
+ * share query/key heads (Hv a multiple of Hk; value head h uses key head
+ * h / (Hv / Hk)) and whose keys and values may differ in width:
+ *   S_t = exp(g_t) (I - beta_t k_t k_t^T) S_{t-1} + beta_t k_t v_t^T,
+ *   o_t = scale * S_t^T q_t,   S a Dk x Dv float32 matrix,
+ * with q and k L2-normalised as in step 2 above under KDA_FLAG_L2NORM_QK.  (The
+ * mixer above has a decay per key channel, equal heads and one head_dim; its
+ * short convolution can run before this one through kda_conv_norm.)
+ *
+ * Decay and write strength as in step 3's options: g and beta are given, or with
+ * A_log and dt_bias (both [Hv]) g holds the raw projection f and the decay is
+ * -exp(A_log[h]) softplus(f + dt_bias[h]); with KDA_FLAG_BETA_LOGITS beta holds
+ * logits.  A given g may be -inf: the state is forgotten before that token.
+ *
+ * Layouts: q, k [B][T][Hk][Dk]; v, o [B][T][Hv][Dv]; g, beta [B][T][Hv];
+ * S0, S_T [B][Hv][Dk][Dv] float32.  q, k, v may be parts of wider rows: q_stride,
+ * k_stride, v_stride are the elements between two tokens (0: packed rows; else at
+ * least the row and a multiple of 16 bytes); q, k, v may overlap one another, so
+ * one fused projection [B][T][row] serves all three.
+ * Packed sequences: cu_seqlens as in kda_prefill (B = 1, offsets clamped; tokens
+ * outside every sequence are left as they were in o and in the gradients).
+ * Supported: Dk and Dv in {32, 64, 128}.  The chunk length is the library's own.
+ */
+typedef struct kda_gdr_args {
+  int32_t B, T, Hk, Hv, Dk, Dv;
+  uint32_t flags;       /* KDA_FLAG_* */
+  float l2_eps;         /* >= 0, finite */
+  float scale;          /* finite */
+  int32_t io;           /* kda_dtype of q, k, v, g, beta, o */
+  int64_t q_stride, k_stride, v_stride; /* elements between tokens; 0 = packed */
+  const void* q;
+  const void* k;
+  const void* v;
+  const void* g;
+  const void* beta;
+  const float* S0;      /* or NULL (= zeros) */
+  void* o;              /* may not overlap any input */
+  float* S_T;           /* may equal S0 */
+  const float* A_log;   /* [Hv], given iff dt_bias is, or NULL */
+  const float* dt_bias;
+  const int32_t* cu_seqlens;
+  int32_t n_seqs;
+} kda_gdr_args;
+
+kda_status kda_validate_gdr_prefill(const kda_gdr_args* a);
+/* Bytes of device workspace (0 if invalid, or if none is needed). */
+size_t kda_gdr_prefill_workspace_bytes(const kda_gdr_args* a);
+/* Enqueue the whole forward.  ws: 256-byte aligned, not shared with a call that
+ * may run concurrently (two captured graphs that may replay at the same time need
+ * one each).  The state and every sum are float32: with bf16 inputs S_T is within
+ * about 1e-6 of an exact computation (relative L2), o within bf16's rounding. */
+kda_status kda_gdr_prefill(const kda_gdr_args* a, void* ws, size_t ws_bytes, void* stream);
+
+/* Gradients of L = <o, dO> + <S_T, dS_T> with respect to q, k, v, g, beta (as
+ * given: of the raw projections and logits with the options) and S0; dq and dk sum
+ * over the value heads that share a key head.  The forward is recomputed; fwd.o
+ * and fwd.S_T are not used and may be NULL.  dq, dk, dv, dg, dbeta are in the I/O
+ * type, packed rows (no strides); the others float32.  No output may overlap an
+ * input or another output. */
+typedef struct kda_gdr_backward_args {
+  kda_gdr_args fwd;
+  const void* dO;       /* [B][T][Hv][Dv] */
+  const float* dS_T;    /* [sequences][Hv][Dk][Dv] or NULL (= zeros) */
+  void* dq;             /* [B][T][Hk][Dk] */
+  void* dk;             /* [B][T][Hk][Dk] */
+  void* dv;             /* [B][T][Hv][Dv] */
+  void* dg;             /* [B][T][Hv] */
+  void* dbeta;          /* [B][T][Hv] */
+  float* dS0;           /* or NULL (not written) */
+  float* dA_log;        /* [Hv] or NULL; NULL without A_log */
+  float* ddt_bias;      /* [Hv] or NULL; NULL without A_log */
+} kda_gdr_backward_args;
+
+kda_status kda_validate_gdr_backward(const kda_gdr_backward_args* a);
+size_t kda_gdr_backward_workspace_bytes(const kda_gdr_backward_args* a);
+kda_status kda_gdr_prefill_backward(const kda_gdr_backward_args* a, void* ws, size_t ws_bytes,
+                                    void* stream);
+
+/* Single tokens on a pool of states, for continuous batching: row i is a token of
+ * the sequence whose state is S[slots[i]], updated in place.  A row whose slot is
+ * outside [0, n_slots) is padding: nothing of it is read and its o is left as it
+ * was.  Rows with the same slot are consecutive tokens of that sequence, in row
+ * order (a few tokens at once cost one pass over the state).  slots NULL: row i
+ * uses slot i (N <= n_slots).
+ * q, k [N][Hk][Dk]; v, o [N][Hv][Dv]; g, beta [N][Hv]; strides as above, between
+ * rows. */
+typedef struct kda_gdr_decode_args {
+  int32_t N, n_slots, Hk, Hv, Dk, Dv;
+  uint32_t flags;
+  float l2_eps;
+  float scale;
+  int32_t io;
+  int64_t q_stride, k_stride, v_stride;
+  const void* q;
+  const void* k;
+  const void* v;
+  const void* g;
+  const void* beta;
+  const float* A_log;
+  const float* dt_bias;
+  float* S;             /* [n_slots][Hv][Dk][Dv] in/out */
+  const int32_t* slots; /* device [N] or NULL */
+  void* o;              /* may not overlap any input */
+} kda_gdr_decode_args;
+
+kda_status kda_validate_gdr_decode(const kda_gdr_decode_args* a);
+kda_status kda_gdr_decode(const kda_gdr_decode_args* a, void* stream);
+
+/* -------------------------------------------------------- pages of a cache */
+/* A pool is memory of n_layers layers (layer_stride bytes apart) with n_pages pages
+ * of page_bytes each (a multiple of 16) -- for the states above one page is one
+ * sequence's state of one layer, for any cache whatever its pages hold.  refs
+ * [n_pages] (int32, device) counts a page's holders; 0 or less is free.  Calls read
+ * refs and write the new counts to refs_out, which may be refs itself; page lists
+ * are device arrays.  Bad indexes in them are never followed.
+ * All calls are deterministic: of several choices the lowest index is taken. */
+typedef struct kda_pages_pool {
+  void* data;
+  int64_t layer_stride; /* bytes; a multiple of 16, >= n_pages * page_bytes (0 = exactly that) */
+  int64_t page_bytes;
+  int32_t n_layers, n_pages;
+} kda_pages_pool;
+
+/* Workspace of fork and copy (n requests) and of compact (n = 0), 256-byte aligned;
+ * 0 if the sizes are invalid. */
+size_t kda_pages_workspace_bytes(const kda_pages_pool* pool, int32_t n);
+
+/* Forks: request i gets a free page (the lowest ones, in request order), filled
+ * with a copy of page src[i] in every layer, or with zeros where src[i] = -1, its
+ * count 1; the page goes to dst[i].  dst[i] = -1 and nothing is taken where src[i]
+ * is no page in use (nor -1) or no free page is left. */
+kda_status kda_pages_fork(const kda_pages_pool* pool, const int32_t* refs, int32_t* refs_out,
+                          const int32_t* src, int32_t* dst, int32_t n, void* ws, size_t ws_bytes,
+                          void* stream);
+
+/* Frees: refs_out = refs, each page's count lowered once for every time pages
+ * lists it (not below 0). */
+kda_status kda_pages_free(const int32_t* refs, int32_t* refs_out, int32_t n_pages,
+                          const int32_t* pages, int32_t n, void* stream);
+
+/* Compaction: with n_used[0] the pages in use, those at n_used[0] and behind move
+ * to the free pages before it, in order; no other page moves.  new_id[p] is page
+ * p's new index (-1 for a free one), table_out[i] = new_id[table[i]] (-1 where
+ * table[i] is no page) for n_table entries (table_out may be table; both NULL if
+ * n_table is 0). */
+kda_status kda_pages_compact(const kda_pages_pool* pool, const int32_t* refs, int32_t* refs_out,
+                             int32_t* new_id, int32_t* n_used, const int32_t* table,
+                             int32_t* table_out, int64_t n_table, void* ws, size_t ws_bytes,
+                             void* stream);
+
+/* Copies page src[i] of one pool to page dst[i] of another or the same one (zeros
+ * where src[i] = -1), n_layers and page_bytes alike.  Pairs outside the pools are
+ * left out, of several pairs with one destination all but the first, and within
+ * one pool every pair whose source is the destination of some pair, so no result
+ * depends on an order; done[i] (or NULL) says 1 for a pair that was copied, else 0.
+ * The two pools' memory is the same or disjoint. */
+kda_status kda_pages_copy(const kda_pages_pool* src_pool, const kda_pages_pool* dst_pool,
+                          const int32_t* src, const int32_t* dst, int32_t* done, int32_t n, void* ws,
+                          size_t ws_bytes, void* stream);
+
 /* ------------------------------------------------------------------- misc */
 const char* kda_status_str(int status);
 int kda_abi_version(void);
