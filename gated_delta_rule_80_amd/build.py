@@ -27,6 +27,10 @@ SOURCES = ["kda_api.cpp", "kda_noalloc.hip", "kda_prep.hip", "kda_prep_exact.hip
            "kda_gdr_api.cpp", "kda_gdr_prep.hip", "kda_gdr_walk.hip",
            "kda_gdr_reverse.hip", "kda_gdr_grad.hip", "kda_gdr_decode.hip", "kda_pages.hip"]
 ARCH = "gfx950"
+# matrix-core accumulators in ordinary registers: the walks use them as vector
+# operands between products, which would cost a move each way otherwise
+EXTRA_FLAGS = {src: ["-mllvm", "-amdgpu-mfma-vgpr-form=1"]
+               for src in ("kda_gdr_walk.hip", "kda_gdr_reverse.hip", "kda_gdr_grad.hip")}
 
 
 def hipcc() -> str:
@@ -45,7 +49,7 @@ def common_flags() -> list[str]:
 def compile_one(src: str) -> str:
     obj = os.path.join(BUILD, os.path.splitext(src)[0] + ".o")
     lang = ["-x", "hip"] if src.endswith(".cpp") else []
-    cmd = [hipcc(), *common_flags(), *lang, "-c", os.path.join(CSRC, src), "-o", obj]
+    cmd = [hipcc(), *common_flags(), *EXTRA_FLAGS.get(src, []), *lang, "-c", os.path.join(CSRC, src), "-o", obj]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"compile failed: {' '.join(cmd)}\n{r.stdout}\n{r.stderr}")

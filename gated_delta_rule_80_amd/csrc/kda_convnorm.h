@@ -33,25 +33,6 @@ __device__ __forceinline__ float softplus_log2(float x) {
   return fmaf(fmaxf(x, 0.0f), kLog2e, __builtin_amdgcn_logf(1.0f + e));
 }
 
-typedef unsigned u32x4 __attribute__((ext_vector_type(4)));
-typedef __amdgpu_buffer_rsrc_t BufRes;
-
-// Buffer resource over `bytes` bytes from `base` (raw, no stride).  Loads through
-// it are range checked: an access at or past `bytes` -- a negative 32-bit offset
-// included -- returns zeros.  The third word selects 32-bit data format, as
-// untyped loads need on gfx9.
-// base and bytes must be the same in every lane; they are moved to scalar
-// registers explicitly (a resource computed in vector registers would otherwise
-// be legalised with a loop over lanes).
-__device__ __forceinline__ BufRes make_buf(const void* base, unsigned bytes) {
-  const unsigned long long a = reinterpret_cast<unsigned long long>(base);
-  const unsigned lo = __builtin_amdgcn_readfirstlane((unsigned)a);
-  const unsigned hi = __builtin_amdgcn_readfirstlane((unsigned)(a >> 32));
-  void* sbase = reinterpret_cast<void*>(((unsigned long long)hi << 32) | lo);
-  return __builtin_amdgcn_make_buffer_rsrc(sbase, (short)0,
-                                           (int)__builtin_amdgcn_readfirstlane(bytes), 0x00020000);
-}
-
 // 8 consecutive elements kept unconverted while their load is in flight.
 template <typename IO> struct Raw8;
 template <> struct Raw8<__bf16> {

@@ -388,6 +388,27 @@ __device__ __forceinline__ int xcd_major(int blk, int n) {
   return x * q + (x < rem ? x : rem) + i;
 }
 
+// ------------------------------------------------------------ buffer accesses
+typedef unsigned u32x4 __attribute__((ext_vector_type(4)));
+typedef __amdgpu_buffer_rsrc_t BufRes;
+
+// Buffer resource over `bytes` bytes from `base` (raw, no stride).  Loads through
+// it are range checked: an access at or past `bytes` -- a negative 32-bit offset
+// included -- returns zeros.  The third word selects 32-bit data format, as
+// untyped loads need on gfx9.
+// Stores past the range are dropped.
+// base and bytes must be the same in every lane; they are moved to scalar
+// registers explicitly (a resource computed in vector registers would otherwise
+// be legalised with a loop over lanes).
+__device__ __forceinline__ BufRes make_buf(const void* base, unsigned bytes) {
+  const unsigned long long a = reinterpret_cast<unsigned long long>(base);
+  const unsigned lo = __builtin_amdgcn_readfirstlane((unsigned)a);
+  const unsigned hi = __builtin_amdgcn_readfirstlane((unsigned)(a >> 32));
+  void* sbase = reinterpret_cast<void*>(((unsigned long long)hi << 32) | lo);
+  return __builtin_amdgcn_make_buffer_rsrc(sbase, (short)0,
+                                           (int)__builtin_amdgcn_readfirstlane(bytes), 0x00020000);
+}
+
 // ------------------------------------------------------------ packed sequences
 // The sequence that owns chunk slot gc: the largest i < n_seqs with cstart[i] <=
 // gc (an empty sequence owns no slot, so it is skipped).  gc < cstart[n_seqs].

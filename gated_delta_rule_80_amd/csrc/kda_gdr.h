@@ -27,27 +27,29 @@ constexpr int gdr_chunk(bool fp32) { return fp32 ? 32 : 64; }
 // One record per (sequence, value head, chunk), element type E:
 //   Tm   [TT][C][C]  row-major, TT terms: bf16 keeps Tm as hi + lo (16 bits of
 //                    mantissa), float32 as it is
-//   P    [PT][C][C]  row-major: one term for the forward, hi + lo (bf16) for the
-//                    backward, whose dS0 leaves in float32
 //   sc   [8][C]      float32, per token: cx = gamma rk, cy = b lambda rk,
-//                    co = scale gamma rq, rk, rq, G (high part), G (low part),
-//                    b; rows behind the sequence's end hold zeros in cx, cy, co,
-//                    rk, rq, b
+//                    co = scale gamma rq, rk, rq, G in log2 units (high part, low
+//                    part), b; rows behind the sequence's end hold zeros in cx,
+//                    cy, co, rk, rq, b
+//   P    [C][C]      forward: one term (its products end in the output)
+// or, for the backward (whose dS0 leaves in float32),
+//   P^T, Tm^T [TT][C][C]  the transposes, rows as the reverse walk reads them
 // where rk, rq are 1 / norm (1 without the normalisation).
 struct GdrRecord {
-  size_t t, p, sc;  // byte offsets
-  size_t bytes;     // 256-byte multiple
+  size_t t, sc, p, tt;  // byte offsets
+  size_t bytes;         // 256-byte multiple
 };
 constexpr int kGdrScalars = 8;
 
 constexpr GdrRecord gdr_record(bool fp32, bool bwd) {
-  const size_t C = (size_t)gdr_chunk(fp32), es = fp32 ? 4 : 2;
-  const size_t tt = fp32 ? 1 : 2, pt = fp32 ? 1 : (bwd ? 2 : 1);
+  const size_t C = (size_t)gdr_chunk(fp32), es = fp32 ? 4 : 2, terms = fp32 ? 1 : 2;
+  const size_t mat = C * C * es;
   GdrRecord r{};
   r.t = 0;
-  r.p = tt * C * C * es;
-  r.sc = r.p + pt * C * C * es;
-  r.bytes = round_up(r.sc + kGdrScalars * C * 4, 256);
+  r.sc = terms * mat;
+  r.p = r.sc + kGdrScalars * C * 4;
+  r.tt = r.p + (bwd ? terms : 1) * mat;
+  r.bytes = round_up(r.tt + (bwd ? terms * mat : 0), 256);
   return r;
 }
 

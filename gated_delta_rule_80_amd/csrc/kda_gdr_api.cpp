@@ -34,9 +34,11 @@ bool rows_bytes(size_t& out, size_t rows, size_t row, int64_t stride, size_t es)
   return true;
 }
 
-// a stride is 0, or holds the row and keeps its 16-byte pieces aligned
+// a stride is 0, or holds the row and keeps its 16-byte pieces aligned; the kernels
+// address the rows of a chunk by 32-bit offsets
 bool stride_ok(int64_t stride, size_t row, size_t es) {
-  return stride == 0 || (stride >= (int64_t)row && (size_t)stride * es % 16 == 0 && stride < (int64_t(1) << 40));
+  return row <= (size_t(1) << 23) &&
+         (stride == 0 || (stride >= (int64_t)row && (size_t)stride * es % 16 == 0 && stride <= (int64_t(1) << 23)));
 }
 
 struct GdrSizes {

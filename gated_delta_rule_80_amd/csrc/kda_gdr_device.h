@@ -117,6 +117,42 @@ __device__ __forceinline__ f32x4 g_colp(const float* img, int u, int tile, int r
   for (int e = 0; e < 4; ++e) f[e] = img[GImg<float, K>::at(16 * u + 4 * g + e, 16 * tile + r)];
   return f;
 }
+// Both units of the two tiles 2 jj, 2 jj + 1 of the columns of a 64-row bf16 image,
+// as the transposing reads with their wait in one block: the compiler has a
+// transposing read that it can see wait for every global-to-LDS copy in flight, the
+// next chunk's included.  The rows' swizzle depends on the lane only, so one
+// address serves all eight reads.
+template <int K>
+__device__ __forceinline__ void g_colp_pair(const __bf16* img, int jj, int r, int g, bf16x8 (&t0)[2], bf16x8 (&t1)[2]) {
+  typedef __attribute__((address_space(3))) const __bf16 lds_bf16;
+  const uint32_t at = (uint32_t)(uintptr_t)(lds_bf16*)(img + GImg<__bf16, K>::at(8 * g + (r >> 2), 32 * jj + 8 * (r & 3)));
+  bf16x4 a, b, c, d, e, f, x, y;
+  asm volatile(
+      "ds_read_b64_tr_b16 %0, %8\n\t"
+      "ds_read_b64_tr_b16 %1, %8 offset:%9\n\t"
+      "ds_read_b64_tr_b16 %2, %8 offset:%10\n\t"
+      "ds_read_b64_tr_b16 %3, %8 offset:%11\n\t"
+      "ds_read_b64_tr_b16 %4, %8 offset:8\n\t"
+      "ds_read_b64_tr_b16 %5, %8 offset:%12\n\t"
+      "ds_read_b64_tr_b16 %6, %8 offset:%13\n\t"
+      "ds_read_b64_tr_b16 %7, %8 offset:%14\n\t"
+      "s_waitcnt lgkmcnt(0)"
+      : "=&v"(a), "=&v"(b), "=&v"(c), "=&v"(d), "=&v"(e), "=&v"(f), "=&v"(x), "=&v"(y)
+      : "v"(at), "n"(4 * K * 2), "n"(32 * K * 2), "n"(36 * K * 2), "n"(4 * K * 2 + 8), "n"(32 * K * 2 + 8),
+        "n"(36 * K * 2 + 8));
+  t0[0] = __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7);
+  t0[1] = __builtin_shufflevector(c, d, 0, 1, 2, 3, 4, 5, 6, 7);
+  t1[0] = __builtin_shufflevector(e, f, 0, 1, 2, 3, 4, 5, 6, 7);
+  t1[1] = __builtin_shufflevector(x, y, 0, 1, 2, 3, 4, 5, 6, 7);
+}
+template <int K>
+__device__ __forceinline__ void g_colp_pair(const float* img, int jj, int r, int g, f32x4 (&t0)[2], f32x4 (&t1)[2]) {
+#pragma unroll
+  for (int u = 0; u < 2; ++u) {
+    t0[u] = g_colp<K>(img, u, 2 * jj, r, g);
+    t1[u] = g_colp<K>(img, u, 2 * jj + 1, r, g);
+  }
+}
 // columns m0 + lane
 template <int K>
 __device__ __forceinline__ bf16x8 g_col(const __bf16* img, int u, int m0, int r, int g) {
@@ -150,21 +186,26 @@ __device__ __forceinline__ f32x4 g_acc(const float* img, int tile, int m0, int r
 
 // NT terms of one unit of a float32 quantity held in accumulators.
 template <typename E, int NT> struct Terms;
+typedef float f32x2 __attribute__((ext_vector_type(2)));
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 template <int NT> struct Terms<__bf16, NT> {
   static constexpr int N = NT;
   bf16x8 t[NT];
   __device__ __forceinline__ void set(const f32x4* tiles) {  // tiles of the unit
-    float x[8];
 #pragma unroll
-    for (int e = 0; e < 4; ++e) { x[e] = tiles[0][e]; x[4 + e] = tiles[1][e]; }
+    for (int q = 0; q < 4; ++q) {  // pairs: one conversion instruction each
+      f32x2 x = {tiles[q >> 1][2 * (q & 1)], tiles[q >> 1][2 * (q & 1) + 1]};
 #pragma unroll
-    for (int n = 0; n < NT; ++n)
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const __bf16 h = (__bf16)x[e];
-        t[n][e] = h;
-        if (n + 1 < NT) x[e] -= (float)h;
+      for (int n = 0; n < NT; ++n) {
+        const bf16x2 h = __builtin_convertvector(x, bf16x2);
+        t[n][2 * q] = h[0];
+        t[n][2 * q + 1] = h[1];
+        if (n + 1 < NT) {
+          x[0] -= (float)h[0];
+          x[1] -= (float)h[1];
+        }
       }
+    }
   }
 };
 template <int NT> struct Terms<float, NT> {
@@ -185,6 +226,64 @@ __device__ __forceinline__ void gmma_terms(f32x4& acc, const F (&a)[AT], const T
       if (i + j < LIM) gmma(acc, a[i], b.t[j]);
 }
 
+// 2^x by the hardware instruction (1 ulp; results below 2^-126 are 0, and so is the
+// decay they stand for to any use)
+__device__ __forceinline__ float exp2_fast(float x) { return __builtin_amdgcn_exp2f(x); }
+
+// A 4 x 4 transpose inside every quad of lanes: x[e] of lane j goes to element j of
+// lane e, rounded to bf16.  Lane q of a quad then holds row q of the tile's 4 rows
+// over 4 consecutive columns: one 8-byte store instead of four of 2 bytes.
+__device__ __forceinline__ uint2 quad_transpose(const f32x4& x, int r) {
+  const bf16x2 a = __builtin_convertvector((f32x2){x[0], x[1]}, bf16x2);
+  const bf16x2 b = __builtin_convertvector((f32x2){x[2], x[3]}, bf16x2);
+  const uint32_t d0 = __builtin_bit_cast(uint32_t, a), d1 = __builtin_bit_cast(uint32_t, b);
+  const uint32_t o0 = (uint32_t)__builtin_amdgcn_mov_dpp((int)d0, 0xB1, 0xF, 0xF, false);  // lane ^ 1
+  const uint32_t o1 = (uint32_t)__builtin_amdgcn_mov_dpp((int)d1, 0xB1, 0xF, 0xF, false);
+  // bytes 0-3 are the second argument's, 4-7 the first's: an even lane takes both
+  // low halves (own first), an odd lane both high halves (own second)
+  const uint32_t sel = (r & 1) ? 0x03020706u : 0x05040100u;
+  const uint32_t p0 = __builtin_amdgcn_perm(o0, d0, sel), p1 = __builtin_amdgcn_perm(o1, d1, sel);
+  const bool up = (r & 2) != 0;
+  const uint32_t got = (uint32_t)__builtin_amdgcn_mov_dpp((int)(up ? p0 : p1), 0x4E, 0xF, 0xF, false);  // lane ^ 2
+  return make_uint2(up ? got : p0, up ? p1 : got);
+}
+
+// Stores through a range-checked buffer (rows behind a sequence's end lie behind the
+// range and are dropped): no branch, and every chunk issues the same number of them.
+typedef unsigned u32x2 __attribute__((ext_vector_type(2)));
+// One accumulator tile of a [row][16 columns] block, rows `ld` bytes apart: rows
+// row0 .. + 3 of column col0 + r (row0 of this lane group), col0 in bytes.
+__device__ __forceinline__ void store_tile(const BufRes& b, int row0, int ld, int col0, const f32x4& x, int r,
+                                           __bf16) {
+  const uint2 y = quad_transpose(x, r);
+  __builtin_amdgcn_raw_buffer_store_b64((u32x2){y.x, y.y}, b, (row0 + (r & 3)) * ld + col0 + 8 * (r >> 2), 0, 0);
+}
+__device__ __forceinline__ void store_tile(const BufRes& b, int row0, int ld, int col0, const f32x4& x, int r,
+                                           float) {
+#pragma unroll
+  for (int e = 0; e < 4; ++e)
+    __builtin_amdgcn_raw_buffer_store_b32(__builtin_bit_cast(unsigned, (float)x[e]), b, (row0 + e) * ld + col0 + 4 * r,
+                                          0, 0);
+}
+// 4 consecutive elements at byte offset `at`
+__device__ __forceinline__ void store_four(const BufRes& b, int at, const f32x4& x, __bf16) {
+  const bf16x2 lo = __builtin_convertvector((f32x2){x[0], x[1]}, bf16x2);
+  const bf16x2 hi = __builtin_convertvector((f32x2){x[2], x[3]}, bf16x2);
+  __builtin_amdgcn_raw_buffer_store_b64((u32x2){__builtin_bit_cast(uint32_t, lo), __builtin_bit_cast(uint32_t, hi)},
+                                        b, at, 0, 0);
+}
+__device__ __forceinline__ void store_four(const BufRes& b, int at, const f32x4& x, float) {
+  __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, x), b, at, 0, 0);
+}
+
+// Values that are the same in every lane, moved to scalar registers.
+__device__ __forceinline__ int uniform(int x) { return __builtin_amdgcn_readfirstlane(x); }
+__device__ __forceinline__ long uniform(long x) {
+  const unsigned lo = __builtin_amdgcn_readfirstlane((unsigned)x);
+  const unsigned hi = __builtin_amdgcn_readfirstlane((unsigned)((unsigned long)x >> 32));
+  return (long)(((unsigned long)hi << 32) | lo);
+}
+
 // One chunk of a walk: where its rows stand and its record.
 struct GdrSpan {
   long tok0;    // first token of the sequence
@@ -202,9 +301,9 @@ __device__ __forceinline__ GdrSpan gdr_span(const GdrShape& s, int b, int h, int
     x.rstride = (size_t)s.B * s.Hv;
     x.rec0 = rec_slot(0, (size_t)b * s.Hv + h, x.rstride);
   } else {
-    x.tok0 = s.seqs.bounds[b];
-    x.Tq = s.seqs.bounds[b + 1] - s.seqs.bounds[b];
-    int c0 = s.seqs.cstart[b];
+    x.tok0 = uniform(s.seqs.bounds[b]);
+    x.Tq = uniform(s.seqs.bounds[b + 1]) - (int)x.tok0;
+    int c0 = uniform(s.seqs.cstart[b]);
     c0 = c0 < 0 ? 0 : (c0 > s.NT ? s.NT : c0);
     const int n = (x.Tq + C - 1) / C;
     x.nch = n < s.NT - c0 ? n : s.NT - c0;
@@ -241,35 +340,52 @@ __device__ __forceinline__ GdrChunk gdr_chunk_at(const GdrShape& s, int slot, in
   return x;
 }
 
-// Copies rows of K elements (16-byte pieces permuted as GImg says) from global
-// memory into an LDS image; rows past the last one read the last one.
+// Copies ROWS rows of K elements (16-byte pieces permuted as GImg says) from global
+// memory into an LDS image, NT threads.  A thread's offsets from the first row do
+// not change from chunk to chunk (32 bits: the host bounds the stride), so a whole
+// chunk costs one load instruction per piece; in a chunk with fewer rows those
+// past the last one read the last one.
 template <int NT, int ROWS, int K, typename IO>
-__device__ __forceinline__ void gdr_copy_rows(char* img, const IO* base, long stride, int last,
-                                              int tid) {
+struct GdrCopy {
   using I = GImg<IO, K>;
-  constexpr int N = ROWS * I::RC;
-  const int wbase = tid & ~63;
-#pragma unroll
-  for (int it = 0; it < (N + NT - 1) / NT; ++it) {
-    const int idx = it * NT + tid;
+  static constexpr int N = ROWS * I::RC, ITERS = (N + NT - 1) / NT;
+  uint32_t off[ITERS];
+  __device__ __forceinline__ static uint32_t offset(int it, uint32_t stride, int last) {
     int row, c;
-    I::source(idx, row, c);
-    row = row < last ? row : last;
-    if (N % NT == 0 || idx < N)
-      __builtin_amdgcn_global_load_lds((const glb_void_t*)(base + row * stride + c * I::EPC),
-                                       (lds_void_t*)(img + (size_t)(it * NT + wbase) * 16), 16, 0, 0);
+    I::source(it * NT + (int)threadIdx.x, row, c);
+    return (uint32_t)(row < last ? row : last) * stride + (uint32_t)c * 16;
   }
-}
+  __device__ __forceinline__ void init(long stride) {
+#pragma unroll
+    for (int it = 0; it < ITERS; ++it) off[it] = offset(it, (uint32_t)(stride * (long)sizeof(IO)), ROWS - 1);
+  }
+  // img, base and wave are the same in every lane
+  __device__ __forceinline__ static void load(char* img, int it, const char* base, uint32_t o, int wave) {
+    if (N % NT == 0 || it * NT + (int)threadIdx.x < N)
+      __builtin_amdgcn_global_load_lds((const glb_void_t*)(base + o),
+                                       (lds_void_t*)(img + (size_t)(it * NT + 64 * wave) * 16), 16, 0, 0);
+  }
+  __device__ __forceinline__ void whole(char* img, const IO* base, int wave) const {
+#pragma unroll
+    for (int it = 0; it < ITERS; ++it) load(img, it, reinterpret_cast<const char*>(base), off[it], wave);
+  }
+  __device__ __forceinline__ void part(char* img, const IO* base, long stride, int last, int wave) const {
+#pragma unroll
+    for (int it = 0; it < ITERS; ++it)
+      load(img, it, reinterpret_cast<const char*>(base), offset(it, (uint32_t)(stride * (long)sizeof(IO)), last),
+           wave);
+  }
+};
+// BYTES consecutive bytes
 template <int NT, int BYTES>
-__device__ __forceinline__ void gdr_copy_flat(char* img, const char* base, int tid) {
+__device__ __forceinline__ void gdr_copy_flat(char* img, const char* base, int wave) {
   constexpr int N = BYTES / 16;
-  const int wbase = tid & ~63;
 #pragma unroll
   for (int it = 0; it < (N + NT - 1) / NT; ++it) {
-    const int idx = it * NT + tid;
-    if (N % NT == 0 || idx < N)
-      __builtin_amdgcn_global_load_lds((const glb_void_t*)(base + (size_t)idx * 16),
-                                       (lds_void_t*)(img + (size_t)(it * NT + wbase) * 16), 16, 0, 0);
+    const uint32_t idx = it * NT + threadIdx.x;
+    if (N % NT == 0 || idx < (uint32_t)N)
+      __builtin_amdgcn_global_load_lds((const glb_void_t*)(base + idx * 16u),
+                                       (lds_void_t*)(img + (size_t)(it * NT + 64 * wave) * 16), 16, 0, 0);
   }
 }
 

@@ -157,8 +157,8 @@ __global__ __launch_bounds__(256) void kda_gdr_grad_kernel(GdrGradParams p) {
 #pragma unroll
     for (int t = 0; t < TW; ++t) {
       const int tk = 16 * (tile0 + t) + r;
-      const float gam = expf(sc[5][tk] + sc[6][tk]);
-      const float lam = expf((GhC - sc[5][tk]) + (GlC - sc[6][tk]));
+      const float gam = exp2_fast(sc[5][tk] + sc[6][tk]);
+      const float lam = exp2_fast((GhC - sc[5][tk]) + (GlC - sc[6][tk]));
       kw1[t] = 0.f;
 #pragma unroll
       for (int c = 0; c < CW; ++c) {
@@ -200,7 +200,7 @@ __global__ __launch_bounds__(256) void kda_gdr_grad_kernel(GdrGradParams p) {
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
             const int j = j4 + e;
-            const float d = j <= i ? expf((sc[5][i] - sc[5][j]) + (sc[6][i] - sc[6][j])) * (sc[7][j] * sc[3][j])
+            const float d = j <= i ? exp2_fast((sc[5][i] - sc[5][j]) + (sc[6][i] - sc[6][j])) * (sc[7][j] * sc[3][j])
                                    : 0.f;
             mo[t][s][e] *= d;
             mx[t][s][e] *= j < i ? -d : 0.f;
@@ -249,7 +249,7 @@ __global__ __launch_bounds__(256) void kda_gdr_grad_kernel(GdrGradParams p) {
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
             const int i = i4 + e;
-            const float d = j <= i ? expf((sc[5][i] - sc[5][j]) + (sc[6][i] - sc[6][j])) : 0.f;
+            const float d = j <= i ? exp2_fast((sc[5][i] - sc[5][j]) + (sc[6][i] - sc[6][j])) : 0.f;
             mo[t][s][e] *= d * (sc[4][i] * p.scale);
             mx[t][s][e] *= j < i ? -d * sc[3][i] : 0.f;
           }
@@ -313,7 +313,7 @@ __global__ __launch_bounds__(256) void kda_gdr_grad_kernel(GdrGradParams p) {
       }
       k1 = group_sum<64>(k1);
       // waves 0 and 2 hold the two channel halves of <S, dS>
-      if (lane == C - 1) dG += expf(GhC + GlC) * (redS[0] + redS[2]) + k1;
+      if (lane == C - 1) dG += exp2_fast(GhC + GlC) * (redS[0] + redS[2]) + k1;
 #pragma unroll
       for (int m = 1; m < C; m <<= 1) {
         const float y = __shfl_down(dG, m, 64);

@@ -14,13 +14,14 @@
 
 namespace kda {
 
-template <int DK, typename IO, int PT>
+template <int DK, typename IO, bool BWD>
 __global__ __launch_bounds__(256) void kda_gdr_prep_kernel(GdrPrepParams p) {
   constexpr bool F32 = sizeof(IO) == 4;
   constexpr int C = gdr_chunk(F32);
   constexpr int NTL = C / 16;                // tiles per side
-  constexpr GdrRecord RF = gdr_record(F32, PT == 2);
+  constexpr GdrRecord R = gdr_record(F32, BWD);
   using I = GImg<IO, DK>;
+  using Frag = typename GOp<IO>::Frag;
   constexpr int RC = I::RC, EPC = I::EPC, NU = DK / GOp<IO>::KU;
   constexpr int LA = C + 4;                  // row stride of the float32 matrices
   constexpr int IMG = C * DK * (int)sizeof(IO);
@@ -29,7 +30,7 @@ __global__ __launch_bounds__(256) void kda_gdr_prep_kernel(GdrPrepParams p) {
   constexpr int BYTES = (2 * IMG > MAT ? 2 * IMG : MAT);
   __shared__ __attribute__((aligned(16))) char lds[BYTES];
   __shared__ __attribute__((aligned(16))) float As[C * LA];
-  __shared__ float sc[kGdrScalars][C];
+  __shared__ __attribute__((aligned(16))) float sc[kGdrScalars][C];
   IO* ik = reinterpret_cast<IO*>(lds);
   IO* iq = reinterpret_cast<IO*>(lds + IMG);
   float* Ts = reinterpret_cast<float*>(lds);
@@ -42,24 +43,22 @@ __global__ __launch_bounds__(256) void kda_gdr_prep_kernel(GdrPrepParams p) {
   const GdrChunk ch = gdr_chunk_at(p.s, slot, b, h, C);
   if (ch.n == 0) return;  // uniform: a slot no sequence owns
 
-  // ---- rows of q and k into LDS, their squared norms on the way
-  for (int idx = tid; idx < 2 * C * RC; idx += 256) {
-    const bool isq = idx >= C * RC;
-    const int i = isq ? idx - C * RC : idx;
-    const int t = i / RC, c = i % RC;
-    const IO* src = isq ? static_cast<const IO*>(p.q) + (ch.tok + t) * p.s.qs
-                        : static_cast<const IO*>(p.k) + (ch.tok + t) * p.s.ks;
-    f32x4 raw = {0.f, 0.f, 0.f, 0.f};
-    if (t < ch.n) raw = *reinterpret_cast<const f32x4*>(src + (size_t)hk * DK + c * EPC);
-    *reinterpret_cast<f32x4*>((isq ? iq : ik) + (t * RC + GOp<IO>::template swz<RC>(t, c)) * EPC) = raw;
-    const IO* x = reinterpret_cast<const IO*>(&raw);
-    float ss = 0.f;
+  // ---- every global load first: the rows of k and q, the gates
+  constexpr int PIECES = C * RC;             // 16-byte pieces of one image
+  constexpr int NL = (PIECES + 255) / 256;
+  f32x4 raw[2][NL];
 #pragma unroll
-    for (int e = 0; e < EPC; ++e) ss = fmaf(to_f32(x[e]), to_f32(x[e]), ss);
-    ss = group_sum<RC>(ss);
-    if (c == 0) sc[isq ? 4 : 3][t] = t < ch.n ? (p.l2 ? 1.0f / sqrtf(ss + p.eps) : 1.0f) : 0.f;
-  }
-  // ---- gates: wave 0, a lane per token
+  for (int x = 0; x < 2; ++x)
+#pragma unroll
+    for (int it = 0; it < NL; ++it) {
+      const int i = it * 256 + tid, t = i / RC, c = i % RC;
+      const IO* src = x ? static_cast<const IO*>(p.q) + (ch.tok + t) * p.s.qs
+                        : static_cast<const IO*>(p.k) + (ch.tok + t) * p.s.ks;
+      raw[x][it] = f32x4{0.f, 0.f, 0.f, 0.f};
+      if ((PIECES % 256 == 0 || i < PIECES) && t < ch.n)
+        raw[x][it] = *reinterpret_cast<const f32x4*>(src + (size_t)hk * DK + c * EPC);
+    }
+  // wave 0, a lane per token: the decay summed in float64, in log2 units
   if (wave == 0) {
     float gt = 0.f, bt = 0.f;
     if (lane < ch.n && lane < C) {
@@ -67,7 +66,7 @@ __global__ __launch_bounds__(256) void kda_gdr_prep_kernel(GdrPrepParams p) {
       gt = gdr_decay<IO>(p.g, at, p.A_log, p.dt_bias, h);
       bt = gdr_beta<IO>(p.beta, at, p.beta_logits);
     }
-    double G = gt;
+    double G = (double)gt * 1.4426950408889634;
 #pragma unroll
     for (int m = 1; m < C; m <<= 1) {
       const double y = __shfl_up(G, m, 64);
@@ -79,54 +78,102 @@ __global__ __launch_bounds__(256) void kda_gdr_prep_kernel(GdrPrepParams p) {
       sc[7][lane] = bt;
     }
   }
+  // ---- rows into LDS, their norms on the way
+#pragma unroll
+  for (int x = 0; x < 2; ++x)
+#pragma unroll
+    for (int it = 0; it < NL; ++it) {
+      const int i = it * 256 + tid, t = i / RC, c = i % RC;
+      if (PIECES % 256 != 0 && i >= PIECES) continue;
+      *reinterpret_cast<f32x4*>((x ? iq : ik) + (t * RC + GOp<IO>::template swz<RC>(t, c)) * EPC) = raw[x][it];
+      const IO* e8 = reinterpret_cast<const IO*>(&raw[x][it]);
+      float ss = 0.f;
+#pragma unroll
+      for (int e = 0; e < EPC; ++e) ss = fmaf(to_f32(e8[e]), to_f32(e8[e]), ss);
+      ss = group_sum<RC>(ss);
+      if (c == 0) sc[x ? 4 : 3][t] = t < ch.n ? (p.l2 ? 1.0f / sqrtf(ss + p.eps) : 1.0f) : 0.f;
+    }
   __syncthreads();
   if (tid < C) {
     const float rk = sc[3][tid], sq = sc[4][tid] * p.scale;
-    const float gam = expf(sc[5][tid] + sc[6][tid]);
-    const float lam = expf((sc[5][C - 1] - sc[5][tid]) + (sc[6][C - 1] - sc[6][tid]));
+    const float gam = exp2_fast(sc[5][tid] + sc[6][tid]);
+    const float lam = exp2_fast((sc[5][C - 1] - sc[5][tid]) + (sc[6][C - 1] - sc[6][tid]));
     sc[0][tid] = gam * rk;
     sc[1][tid] = sc[7][tid] * lam * rk;
     sc[2][tid] = gam * sq;
   }
-  __syncthreads();
 
-  char* rec = p.rec + ch.rec * RF.bytes;
-  IO* recP = reinterpret_cast<IO*>(rec + RF.p);
-  // ---- a and P, tile by tile of the lower triangle
-#pragma unroll 1
-  for (int it = wave; it < NTL * NTL; it += 4) {
-    const int ti = it / NTL, tj = it % NTL;
-    if (tj > ti) {
-      // the upper half of a diagonal 32 x 32 block is read as part of its rows
-      if ((ti >> 1) == (tj >> 1))
-#pragma unroll
-        for (int n = 0; n < PT; ++n)
-#pragma unroll
-          for (int e = 0; e < 4; ++e)
-            recP[(size_t)n * C * C + (16 * ti + 4 * g4 + e) * C + 16 * tj + r] = from_f32<IO>(0.f);
-      continue;
-    }
-    f32x4 kk = {0.f, 0.f, 0.f, 0.f}, qk = {0.f, 0.f, 0.f, 0.f};
+  char* rec = p.rec + ch.rec * R.bytes;
+  IO* recP = reinterpret_cast<IO*>(rec + R.p);
+  // ---- a and P: wave w takes the tiles of row tile w (below it, of column tile w).
+  // Both are formed so that a lane holds 4 consecutive elements of a row of what is
+  // stored: a by rows, P by rows (forward) or by columns (backward, which reads P^T).
+  Frag fw[NU], fx[NU];  // this wave's rows of k; of q (forward: rows i) or k (columns j)
+  if (wave < NTL) {
 #pragma unroll
     for (int u = 0; u < NU; ++u) {
-      const auto fb = g_row<IO, DK>(ik, 16 * tj + r, u, g4);
-      gmma(kk, g_row<IO, DK>(ik, 16 * ti + r, u, g4), fb);
-      gmma(qk, g_row<IO, DK>(iq, 16 * ti + r, u, g4), fb);
+      fw[u] = g_row<IO, DK>(ik, 16 * wave + r, u, g4);
+      if constexpr (!BWD) fx[u] = g_row<IO, DK>(iq, 16 * wave + r, u, g4);
     }
-    const int j = 16 * tj + r;
-    const float ghj = sc[5][j], glj = sc[6][j], bj = sc[7][j] * sc[3][j];
+    // a, rows i = 16 wave + r: lanes hold columns j = 16 tj + 4 g4 ..
+    const int i = 16 * wave + r;
+    const float gi = sc[5][i], li = sc[6][i], ri = sc[3][i], si = sc[4][i] * p.scale, bi = sc[7][i];
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const int i = 16 * ti + 4 * g4 + e;
-      float d = (sc[5][i] - ghj) + (sc[6][i] - glj);
-      d = i >= j ? expf(d) * bj : 0.f;
-      As[i * LA + j] = i > j ? d * sc[3][i] * kk[e] : 0.f;
-      float pv = i >= j ? d * (sc[4][i] * p.scale) * qk[e] : 0.f;
+    for (int tj = 0; tj < NTL; ++tj) {
+      if (tj > wave) {
+        // the upper half of a diagonal 32 x 32 block is read as part of its rows
+        if (!BWD && (tj >> 1) == (wave >> 1)) store4(recP + i * C + 16 * tj + 4 * g4, 0.f, 0.f, 0.f, 0.f);
+        continue;
+      }
+      f32x4 kk = {0.f, 0.f, 0.f, 0.f}, qk = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-      for (int n = 0; n < PT; ++n) {
-        const IO hi = from_f32<IO>(pv);
-        recP[(size_t)n * C * C + i * C + j] = hi;
-        pv -= to_f32(hi);
+      for (int u = 0; u < NU; ++u) {
+        const Frag fj = tj == wave ? fw[u] : g_row<IO, DK>(ik, 16 * tj + r, u, g4);
+        gmma(kk, fj, fw[u]);
+        if constexpr (!BWD) gmma(qk, fj, fx[u]);
+      }
+      const int j = 16 * tj + 4 * g4;
+      const f32x4 gj = *reinterpret_cast<const f32x4*>(&sc[5][j]), lj = *reinterpret_cast<const f32x4*>(&sc[6][j]),
+                  rj = *reinterpret_cast<const f32x4*>(&sc[3][j]), bj = *reinterpret_cast<const f32x4*>(&sc[7][j]);
+      f32x4 av, pv;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const float d = exp2_fast((gi - gj[e]) + (li - lj[e])) * (bj[e] * rj[e]);
+        av[e] = i > j + e ? d * ri * kk[e] : 0.f;
+        pv[e] = i >= j + e ? d * si * qk[e] : 0.f;
+      }
+      *reinterpret_cast<f32x4*>(&As[i * LA + j]) = av;
+      if constexpr (!BWD) store4(recP + i * C + j, pv[0], pv[1], pv[2], pv[3]);
+    }
+    if constexpr (BWD) {
+      // P^T, rows j = 16 wave + r: lanes hold i = 16 ti + 4 g4 ..
+      const int j = i;
+      const float bj = bi * ri;
+#pragma unroll
+      for (int ti = 0; ti < NTL; ++ti) {
+        IO* to = recP + j * C + 16 * ti + 4 * g4;
+        if (ti < wave) {
+          if ((ti >> 1) == (wave >> 1)) {
+            store4(to, 0.f, 0.f, 0.f, 0.f);
+            if constexpr (!F32) store4(to + C * C, 0.f, 0.f, 0.f, 0.f);
+          }
+          continue;
+        }
+        f32x4 qk = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int u = 0; u < NU; ++u) gmma(qk, g_row<IO, DK>(iq, 16 * ti + r, u, g4), fw[u]);
+        const int i4 = 16 * ti + 4 * g4;
+        const f32x4 g_i = *reinterpret_cast<const f32x4*>(&sc[5][i4]), l_i = *reinterpret_cast<const f32x4*>(&sc[6][i4]),
+                    s_i = *reinterpret_cast<const f32x4*>(&sc[4][i4]);
+        float pv[4], lo[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const float d = exp2_fast((g_i[e] - gi) + (l_i[e] - li)) * bj;
+          pv[e] = i4 + e >= j ? d * (s_i[e] * p.scale) * qk[e] : 0.f;
+          lo[e] = pv[e] - to_f32(from_f32<IO>(pv[e]));
+        }
+        store4(to, pv[0], pv[1], pv[2], pv[3]);
+        if constexpr (!F32) store4(to + C * C, lo[0], lo[1], lo[2], lo[3]);
       }
     }
   }
@@ -154,20 +201,20 @@ __global__ __launch_bounds__(256) void kda_gdr_prep_kernel(GdrPrepParams p) {
   }
   __syncthreads();
   // ---- and the blocks below them
-#pragma unroll 1
+#pragma unroll
   for (int d = 1; d < NTL; ++d) {
     const int i = d + wave, j = wave;
     if (i < NTL) {
+      const f32x4 fi = *reinterpret_cast<const f32x4*>(Ts + (16 * i + r) * LA + 16 * i + 4 * g4);
       f32x4 acc = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll 1
-      for (int k = j; k < i; ++k) {
-        const f32x4 fa = *reinterpret_cast<const f32x4*>(As + (16 * i + r) * LA + 16 * k + 4 * g4);
+#pragma unroll
+      for (int k = 0; k < d; ++k) {
+        const f32x4 fa = *reinterpret_cast<const f32x4*>(As + (16 * i + r) * LA + 16 * (j + k) + 4 * g4);
         f32x4 fb;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) fb[e] = Ts[(16 * k + 4 * g4 + e) * LA + 16 * j + r];
+        for (int e = 0; e < 4; ++e) fb[e] = Ts[(16 * (j + k) + 4 * g4 + e) * LA + 16 * j + r];
         gmma(acc, fa, fb);
       }
-      const f32x4 fi = *reinterpret_cast<const f32x4*>(Ts + (16 * i + r) * LA + 16 * i + 4 * g4);
       f32x4 t = {0.f, 0.f, 0.f, 0.f};
       gmma(t, fi, acc);
 #pragma unroll
@@ -175,27 +222,30 @@ __global__ __launch_bounds__(256) void kda_gdr_prep_kernel(GdrPrepParams p) {
     }
     __syncthreads();
   }
-  // ---- Tm and the scalars to the record
-  IO* recT = reinterpret_cast<IO*>(rec + RF.t);
-  for (int idx = tid; idx < C * C / EPC; idx += 256) {
-    const int i = idx / (C / EPC), j = idx % (C / EPC) * EPC;
-    float x[EPC];
+  // ---- Tm (for the backward also Tm^T) and the scalars to the record
 #pragma unroll
-    for (int e = 0; e < EPC; ++e) x[e] = (j >> 4) <= (i >> 4) ? Ts[i * LA + j + e] : 0.f;
-    if constexpr (F32) {
-      *reinterpret_cast<f32x4*>(recT + i * C + j) = f32x4{x[0], x[1], x[2], x[3]};
-    } else {
-      bf16x8 hi, lo;
+  for (int n = 0; n < (BWD ? 2 : 1); ++n) {
+    IO* to = reinterpret_cast<IO*>(rec + (n ? R.tt : R.t));
+    for (int idx = tid; idx < C * C / EPC; idx += 256) {
+      // n = 1: consecutive threads take consecutive columns of Tm, so that their
+      // reads down a column fall into different banks
+      const int i = n ? idx % C : idx / (C / EPC), j = (n ? idx / C : idx % (C / EPC)) * EPC;
+      const bool in = n ? (j >> 4) >= (i >> 4) : (j >> 4) <= (i >> 4);
+      float x[EPC];
 #pragma unroll
-      for (int e = 0; e < EPC; ++e) {
-        hi[e] = (__bf16)x[e];
-        lo[e] = (__bf16)(x[e] - (float)hi[e]);
+      for (int e = 0; e < EPC; ++e) x[e] = in ? (n ? Ts[(j + e) * LA + i] : Ts[i * LA + j + e]) : 0.f;
+      if constexpr (F32) {
+        *reinterpret_cast<f32x4*>(to + i * C + j) = f32x4{x[0], x[1], x[2], x[3]};
+      } else {
+        float lo[8];
+#pragma unroll
+        for (int e = 0; e < EPC; ++e) lo[e] = x[e] - (float)(__bf16)x[e];
+        store8(to + i * C + j, x);
+        store8(to + C * C + i * C + j, lo);
       }
-      *reinterpret_cast<bf16x8*>(recT + i * C + j) = hi;
-      *reinterpret_cast<bf16x8*>(recT + C * C + i * C + j) = lo;
     }
   }
-  float* recS = reinterpret_cast<float*>(rec + RF.sc);
+  float* recS = reinterpret_cast<float*>(rec + R.sc);
   for (int idx = tid; idx < kGdrScalars * C; idx += 256) recS[idx] = sc[idx / C][idx % C];
 }
 
@@ -203,12 +253,11 @@ template <typename IO>
 static hipError_t launch_prep_t(const GdrPrepParams& p, int Dk, bool bwd, hipStream_t st) {
   const unsigned grid = (unsigned)((size_t)p.s.B * p.s.Hv * p.s.NT);
   if (grid == 0) return hipSuccess;
-  constexpr int PB = sizeof(IO) == 4 ? 1 : 2;
 #define KDA_GDR_PREP(D)                                                                          \
   if (bwd)                                                                                       \
-    hipLaunchKernelGGL((kda_gdr_prep_kernel<D, IO, PB>), dim3(grid), dim3(256), 0, st, p);       \
+    hipLaunchKernelGGL((kda_gdr_prep_kernel<D, IO, true>), dim3(grid), dim3(256), 0, st, p);       \
   else                                                                                           \
-    hipLaunchKernelGGL((kda_gdr_prep_kernel<D, IO, 1>), dim3(grid), dim3(256), 0, st, p);        \
+    hipLaunchKernelGGL((kda_gdr_prep_kernel<D, IO, false>), dim3(grid), dim3(256), 0, st, p);        \
   break
   switch (Dk) {
     case 32: KDA_GDR_PREP(32);

@@ -35,11 +35,12 @@ __global__ __launch_bounds__(64 * WV) void kda_gdr_reverse_kernel(GdrReversePara
   constexpr int C = L::C, NT = 64 * WV, VB = 16 * WV;
   constexpr int CT = DK / 16, TL = C / 16;
   constexpr int NUK = DK / Op::KU, NUC = C / Op::KU;
-  constexpr int TPU = Op::TPU, TT = L::TT;
+  constexpr int TPU = Op::TPU, TT = L::TT, ES = L::ES;
   constexpr GdrRecord R = gdr_record(F32, true);
+  constexpr int NSTORE = (F32 ? 4 : 1) * (CT + TL);  // stores of a chunk
   __shared__ __attribute__((aligned(16))) char lds[2 * L::BYTES];
 
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, r = lane & 15, g4 = lane >> 4;
+  const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6), r = lane & 15, g4 = lane >> 4;
   int bh, vblk;
   gdr_walk_id(Dv / VB, bh, vblk);
   const int h = bh % p.s.Hv, b = bh / p.s.Hv, hk = h / (p.s.Hv / p.s.Hk);
@@ -51,33 +52,54 @@ __global__ __launch_bounds__(64 * WV) void kda_gdr_reverse_kernel(GdrReversePara
   const IO* qb = static_cast<const IO*>(p.q) + sp.tok0 * p.s.qs + (size_t)hk * DK;
   const IO* ob = static_cast<const IO*>(p.dO) + sp.tok0 * HD + (size_t)h * Dv + vblk * VB;
 
+  GdrCopy<NT, C, DK, IO> ck, cq;
+  GdrCopy<NT, C, VB, IO> co;
+  GdrCopy<NT, TT * C, C, IO> ct;
+  ck.init(p.s.ks);
+  cq.init(p.s.qs);
+  co.init(HD);
+  ct.init(C);
   auto copy = [&](int n, char* buf) {
     const int last = sp.Tq - n * C - 1;
     const long t0 = (long)n * C;
     const char* rec = p.rec + (sp.rec0 + n * sp.rstride) * R.bytes;
-    gdr_copy_rows<NT, C, DK, IO>(buf + L::K, kb + t0 * p.s.ks, p.s.ks, last, tid);
-    gdr_copy_rows<NT, C, DK, IO>(buf + L::Q, qb + t0 * p.s.qs, p.s.qs, last, tid);
-    gdr_copy_rows<NT, TT * C, C, IO>(buf + L::T, reinterpret_cast<const IO*>(rec + R.t), C, TT * C, tid);
-    gdr_copy_rows<NT, TT * C, C, IO>(buf + L::P, reinterpret_cast<const IO*>(rec + R.p), C, TT * C, tid);
-    gdr_copy_rows<NT, C, VB, IO>(buf + L::DO, ob + t0 * HD, HD, last, tid);
-    gdr_copy_flat<NT, kGdrScalars * C * 4>(buf + L::SC, rec + R.sc, tid);
+    const IO* pk = kb + t0 * p.s.ks;
+    const IO* pq = qb + t0 * p.s.qs;
+    const IO* po = ob + t0 * HD;
+    if (last >= C - 1) {
+      ck.whole(buf + L::K, pk, wave);
+      cq.whole(buf + L::Q, pq, wave);
+      co.whole(buf + L::DO, po, wave);
+    } else {
+      ck.part(buf + L::K, pk, p.s.ks, last, wave);
+      cq.part(buf + L::Q, pq, p.s.qs, last, wave);
+      co.part(buf + L::DO, po, HD, last, wave);
+    }
+    ct.whole(buf + L::T, reinterpret_cast<const IO*>(rec + R.tt), wave);
+    ct.whole(buf + L::P, reinterpret_cast<const IO*>(rec + R.p), wave);
+    gdr_copy_flat<NT, kGdrScalars * C * 4>(buf + L::SC, rec + R.sc, wave);
   };
 
   f32x4 dS[CT];
   const size_t sbase = (size_t)bh * DK * Dv + v0 + r;
 #pragma unroll
-  for (int t = 0; t < CT; ++t)
+  for (int t = 0; t < CT; ++t) dS[t] = f32x4{0.f, 0.f, 0.f, 0.f};
+  if (p.dS_T != nullptr) {
 #pragma unroll
-    for (int e = 0; e < 4; ++e)
-      dS[t][e] = p.dS_T != nullptr ? p.dS_T[sbase + (size_t)(Op::row4(t, g4) + e) * Dv] : 0.f;
+    for (int t = 0; t < CT; ++t)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) dS[t][e] = p.dS_T[sbase + (size_t)(Op::row4(t, g4) + e) * Dv];
+  }
 
   if (sp.nch > 0) copy(sp.nch - 1, lds);
+  __builtin_amdgcn_s_waitcnt(0);  // the first chunk's copies have no stores behind them
 #pragma unroll 1
   for (int n = sp.nch - 1, ib = 0; n >= 0; --n, ib ^= 1) {
     char* buf = lds + ib * L::BYTES;
-    __builtin_amdgcn_s_waitcnt(0);
+    // as in the forward walk: the copies of chunk n have landed, the stores of
+    // chunk n + 1 may be in flight
+    wait_vmcnt<NSTORE>();
     lds_barrier();
-    if (n > 0) copy(n - 1, lds + (ib ^ 1) * L::BYTES);
 
     const IO* iK = reinterpret_cast<const IO*>(buf + L::K);
     const IO* iQ = reinterpret_cast<const IO*>(buf + L::Q);
@@ -86,97 +108,145 @@ __global__ __launch_bounds__(64 * WV) void kda_gdr_reverse_kernel(GdrReversePara
     const IO* iO = reinterpret_cast<const IO*>(buf + L::DO);
     const float* sc = reinterpret_cast<const float*>(buf + L::SC);
 
-    IO* ck = static_cast<IO*>(p.ckpt) + (sp.rec0 + n * sp.rstride) * (size_t)DK * Dv +
-             (size_t)(v0 / 16) * DK * 16 + r;
+    // reads one group of products ahead, as in the forward walk
+    constexpr int HT = TL / 2;
+    auto rows = [&](Frag (&f)[HT][NUK], int t0) {
 #pragma unroll
-    for (int t = 0; t < CT; ++t)
+      for (int t = 0; t < HT; ++t)
 #pragma unroll
-      for (int e = 0; e < 4; ++e) ck[(Op::row4(t, g4) + e) * 16] = from_f32<IO>(dS[t][e]);
-
-    // ---- dO in the accumulators' layout; one term holds a bf16 dO exactly
-    f32x4 dO[TL];
+        for (int u = 0; u < NUK; ++u) f[t][u] = g_row<IO, DK>(iK, Op::perm(t0 + t, r), u, g4);
+    };
+    f32x4 dO[TL];  // in the accumulators' layout (one term holds a bf16 dO exactly)
+    Frag ka[HT][NUK], kc[HT][NUK];
+    rows(ka, 0);
 #pragma unroll
-    for (int t = 0; t < TL; ++t) dO[t] = g_acc<VB>(iO, t, 16 * wave, r, g4);
-    Terms<IO, 1> o1[NUC];
+    for (int t = 0; t < TL; ++t) dO[t] = g_acc<VB>(iO, t, 16 * wave, r, g4);  // before the copies are issued
+    __builtin_amdgcn_sched_barrier(0);
+    if (n > 0) copy(n - 1, lds + (ib ^ 1) * L::BYTES);
+    __builtin_amdgcn_sched_barrier(0);  // the stores counted above come after the copies
+    {
+      const BufRes to = make_buf(static_cast<IO*>(p.ckpt) + (sp.rec0 + n * sp.rstride) * (size_t)DK * Dv,
+                                 (unsigned)(DK * Dv * ES));
 #pragma unroll
-    for (int u = 0; u < NUC; ++u) o1[u].set(&dO[TPU * u]);
+      for (int t = 0; t < CT; ++t)
+        store_tile(to, Op::row4(t, g4), 16 * ES, v0 * DK * ES, dS[t], r, IO{});
+    }
     // ---- dY = cy (K dS) + P^T dO
     Terms<IO, 2> s2[NUK];
 #pragma unroll
     for (int u = 0; u < NUK; ++u) s2[u].set(&dS[TPU * u]);
+    Terms<IO, 1> o1[NUC];
+#pragma unroll
+    for (int u = 0; u < NUC; ++u) o1[u].set(&dO[TPU * u]);
     f32x4 dY[TL];
+    auto k_s = [&](const Frag (&f)[HT][NUK], int t0) {
 #pragma unroll
-    for (int t = 0; t < TL; ++t) {
-      f32x4 acc = {0.f, 0.f, 0.f, 0.f};
+      for (int t = 0; t < HT; ++t) dY[t0 + t] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-      for (int u = 0; u < NUK; ++u) {
-        const Frag fk[1] = {g_row<IO, DK>(iK, Op::perm(t, r), u, g4)};
-        gmma_terms<1>(acc, fk, s2[u]);
+      for (int u = 0; u < NUK; ++u)
+#pragma unroll
+        for (int i = 0; i < s2[u].N; ++i)
+#pragma unroll
+          for (int t = 0; t < HT; ++t) gmma(dY[t0 + t], f[t][u], s2[u].t[i]);
+#pragma unroll
+      for (int t = t0; t < t0 + HT; ++t) {
+        const f32x4 cy = *reinterpret_cast<const f32x4*>(sc + C + Op::row4(t, g4));
+#pragma unroll
+        for (int e = 0; e < 4; ++e) dY[t][e] *= cy[e];
       }
-      const f32x4 cy = *reinterpret_cast<const f32x4*>(sc + C + Op::row4(t, g4));
+    };
+    // the upper triangles of units of P^T and Tm^T
+    constexpr int NF = NUC * (NUC + 1) / 2 * TPU;
+    Frag fT[NF][TT], fP[NF][TT];
+    auto tri = [&](Frag (&f)[NF][TT], const IO* img) {
+      int i = 0;
 #pragma unroll
-      for (int e = 0; e < 4; ++e) acc[e] *= cy[e];
+      for (int t = 0; t < TL; ++t)
 #pragma unroll
-      for (int u = t / TPU; u < NUC; ++u)
+        for (int u = t / TPU; u < NUC; ++u, ++i)
 #pragma unroll
-        for (int i = 0; i < TT; ++i) gmma(acc, g_colp<C>(iP + i * C * C, u, t, r, g4), o1[u].t[0]);
-      dY[t] = acc;
+          for (int k = 0; k < TT; ++k) f[i][k] = g_row<IO, C>(img + k * C * C, Op::perm(t, r), u, g4);
+    };
+    rows(kc, HT);
+    __builtin_amdgcn_sched_barrier(0);
+    k_s(ka, 0);
+    tri(fP, iP);
+    __builtin_amdgcn_sched_barrier(0);
+    k_s(kc, HT);
+    tri(fT, iT);
+    __builtin_amdgcn_sched_barrier(0);
+    {
+      int i = 0;
+#pragma unroll
+      for (int t = 0; t < TL; ++t)
+#pragma unroll
+        for (int u = t / TPU; u < NUC; ++u, ++i)
+#pragma unroll
+          for (int k = 0; k < TT; ++k) gmma(dY[t], fP[i][k], o1[u].t[0]);
     }
     // ---- dX = Tm^T dY
     Terms<IO, 3> y3[NUC];
 #pragma unroll
     for (int u = 0; u < NUC; ++u) y3[u].set(&dY[TPU * u]);
     f32x4 dX[TL];
+    {
+      int i = 0;
 #pragma unroll
-    for (int t = 0; t < TL; ++t) {
-      dX[t] = f32x4{0.f, 0.f, 0.f, 0.f};
+      for (int t = 0; t < TL; ++t) {
+        dX[t] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-      for (int u = t / TPU; u < NUC; ++u) {
-        Frag ft[TT];
-#pragma unroll
-        for (int i = 0; i < TT; ++i) ft[i] = g_colp<C>(iT + i * C * C, u, t, r, g4);
-        gmma_terms<TT>(dX[t], ft, y3[u]);
+        for (int u = t / TPU; u < NUC; ++u, ++i) gmma_terms<TT>(dX[t], fT[i], y3[u]);
       }
     }
+    // ---- dS = gamma_C dS + Q^T (co dO) - K^T (cx dX); the first while dX forms
 #pragma unroll
-    for (int t = 0; t < TL; ++t)
+    for (int t = 0; t < TL; ++t) {
+      const f32x4 co = *reinterpret_cast<const f32x4*>(sc + 2 * C + Op::row4(t, g4));
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const int tt = n * C + Op::row4(t, g4) + e;
-        if (tt < sp.Tq)
-          static_cast<IO*>(p.dv)[(size_t)(sp.tok0 + tt) * HD + (size_t)h * Dv + v0 + r] =
-              from_f32<IO>(dX[t][e]);
+      for (int e = 0; e < 4; ++e) dO[t][e] *= co[e];
+    }
+    Terms<IO, 3> o3[NUC];
+#pragma unroll
+    for (int u = 0; u < NUC; ++u) o3[u].set(&dO[TPU * u]);
+    const float lamC = exp2_fast(sc[5 * C + C - 1] + sc[6 * C + C - 1]);
+#pragma unroll
+    for (int t = 0; t < CT; ++t)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) dS[t][e] *= lamC;
+    auto add_t = [&](const IO* img, const Terms<IO, 3> (&x)[NUC]) {
+#pragma unroll
+      for (int jj = 0; jj < CT / 2; ++jj) {
+        Frag f0[NUC], f1[NUC];
+        g_colp_pair<DK>(img, jj, r, g4, f0, f1);
+#pragma unroll
+        for (int u = 0; u < NUC; ++u)
+#pragma unroll
+          for (int k = 0; k < x[u].N; ++k) {
+            gmma(dS[2 * jj], f0[u], x[u].t[k]);
+            gmma(dS[2 * jj + 1], f1[u], x[u].t[k]);
+          }
       }
-    // ---- dS = gamma_C dS + Q^T (co dO) - K^T (cx dX)
-    const float lamC = expf(sc[5 * C + C - 1] + sc[6 * C + C - 1]);
+    };
+    add_t(iQ, o3);
+    {
+      // rows behind the sequence's end lie behind the buffer
+      const int left = sp.Tq - n * C < C ? sp.Tq - n * C : C;
+      const BufRes to = make_buf(static_cast<IO*>(p.dv) + (size_t)(sp.tok0 + n * C) * HD,
+                                 (unsigned)(left * (int)HD * ES));
+#pragma unroll
+      for (int t = 0; t < TL; ++t)
+        store_tile(to, Op::row4(t, g4), (int)HD * ES, (h * Dv + v0) * ES, dX[t], r, IO{});
+    }
 #pragma unroll
     for (int t = 0; t < TL; ++t) {
       const f32x4 cx = *reinterpret_cast<const f32x4*>(sc + Op::row4(t, g4));
-      const f32x4 co = *reinterpret_cast<const f32x4*>(sc + 2 * C + Op::row4(t, g4));
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        dX[t][e] *= -cx[e];
-        dO[t][e] *= co[e];
-      }
+      for (int e = 0; e < 4; ++e) dX[t][e] *= -cx[e];
     }
-    Terms<IO, 3> x3[NUC], o3[NUC];
+    Terms<IO, 3> x3[NUC];
 #pragma unroll
-    for (int u = 0; u < NUC; ++u) {
-      x3[u].set(&dX[TPU * u]);
-      o3[u].set(&dO[TPU * u]);
-    }
-#pragma unroll
-    for (int t = 0; t < CT; ++t) {
-#pragma unroll
-      for (int e = 0; e < 4; ++e) dS[t][e] *= lamC;
-#pragma unroll
-      for (int u = 0; u < NUC; ++u) {
-        const Frag fk[1] = {g_colp<DK>(iK, u, t, r, g4)};
-        gmma_terms<1>(dS[t], fk, x3[u]);
-        const Frag fq[1] = {g_colp<DK>(iQ, u, t, r, g4)};
-        gmma_terms<1>(dS[t], fq, o3[u]);
-      }
-    }
+    for (int u = 0; u < NUC; ++u) x3[u].set(&dX[TPU * u]);
+    add_t(iK, x3);
   }
   if (p.dS0 != nullptr) {
 #pragma unroll

@@ -39,11 +39,14 @@ __global__ __launch_bounds__(64 * WV) void kda_gdr_walk_kernel(GdrWalkParams p, 
   constexpr int C = L::C, NT = 64 * WV, VB = 16 * WV;
   constexpr int CT = DK / 16, TL = C / 16;             // tiles of the state and of the tokens
   constexpr int NUK = DK / Op::KU, NUC = C / Op::KU;   // contraction units
-  constexpr int TPU = Op::TPU, TT = L::TT;
+  constexpr int TPU = Op::TPU, TT = L::TT, ES = L::ES;
   constexpr GdrRecord R = gdr_record(F32, CK);
+  // stores of a chunk: o, 4 columns each; or the state and Y
+  constexpr int NSTORE = OUT ? TL : (F32 ? 4 : 1) * (CT + TL);
+  static_assert(OUT != CK, "the stores are counted for one or the other");
   __shared__ __attribute__((aligned(16))) char lds[2 * L::BYTES];
 
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, r = lane & 15, g4 = lane >> 4;
+  const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6), r = lane & 15, g4 = lane >> 4;
   int bh, vblk;
   gdr_walk_id(Dv / VB, bh, vblk);
   const int h = bh % p.s.Hv, b = bh / p.s.Hv, hk = h / (p.s.Hv / p.s.Hk);
@@ -55,39 +58,63 @@ __global__ __launch_bounds__(64 * WV) void kda_gdr_walk_kernel(GdrWalkParams p, 
   const IO* qb = static_cast<const IO*>(p.q) + sp.tok0 * p.s.qs + (size_t)hk * DK;
   const IO* vb = static_cast<const IO*>(p.v) + sp.tok0 * p.s.vs + (size_t)h * Dv + vblk * VB;
 
+  GdrCopy<NT, C, DK, IO> ck, cq;
+  GdrCopy<NT, C, VB, IO> cv;
+  GdrCopy<NT, TT * C, C, IO> ct;
+  GdrCopy<NT, C, C, IO> cp;
+  ck.init(p.s.ks);
+  cv.init(p.s.vs);
+  ct.init(C);
+  if constexpr (OUT) {
+    cq.init(p.s.qs);
+    cp.init(C);
+  }
   auto copy = [&](int n, char* buf) {
     const int last = sp.Tq - n * C - 1;  // >= 0: the chunk exists
     const long t0 = (long)n * C;
     const char* rec = p.rec + (sp.rec0 + n * sp.rstride) * R.bytes;
-    gdr_copy_rows<NT, C, DK, IO>(buf + L::K, kb + t0 * p.s.ks, p.s.ks, last, tid);
-    gdr_copy_rows<NT, C, VB, IO>(buf + L::V, vb + t0 * p.s.vs, p.s.vs, last, tid);
-    gdr_copy_rows<NT, TT * C, C, IO>(buf + L::T, reinterpret_cast<const IO*>(rec + R.t), C, TT * C, tid);
-    gdr_copy_flat<NT, kGdrScalars * C * 4>(buf + L::SC, rec + R.sc, tid);
-    if constexpr (OUT) {
-      gdr_copy_rows<NT, C, DK, IO>(buf + L::Q, qb + t0 * p.s.qs, p.s.qs, last, tid);
-      gdr_copy_rows<NT, C, C, IO>(buf + L::P, reinterpret_cast<const IO*>(rec + R.p), C, C, tid);
+    const IO* pk = kb + t0 * p.s.ks;
+    const IO* pq = qb + t0 * p.s.qs;
+    const IO* pv = vb + t0 * p.s.vs;
+    if (last >= C - 1) {
+      ck.whole(buf + L::K, pk, wave);
+      cv.whole(buf + L::V, pv, wave);
+      if constexpr (OUT) cq.whole(buf + L::Q, pq, wave);
+    } else {
+      ck.part(buf + L::K, pk, p.s.ks, last, wave);
+      cv.part(buf + L::V, pv, p.s.vs, last, wave);
+      if constexpr (OUT) cq.part(buf + L::Q, pq, p.s.qs, last, wave);
     }
+    ct.whole(buf + L::T, reinterpret_cast<const IO*>(rec + R.t), wave);
+    if constexpr (OUT) cp.whole(buf + L::P, reinterpret_cast<const IO*>(rec + R.p), wave);
+    gdr_copy_flat<NT, kGdrScalars * C * 4>(buf + L::SC, rec + R.sc, wave);
   };
 
   // ---- initial state
   f32x4 S[CT];
   const size_t sbase = (size_t)bh * DK * Dv + v0 + r;
 #pragma unroll
-  for (int t = 0; t < CT; ++t)
+  for (int t = 0; t < CT; ++t) S[t] = f32x4{0.f, 0.f, 0.f, 0.f};
+  if (p.S0 != nullptr) {
 #pragma unroll
-    for (int e = 0; e < 4; ++e)
-      S[t][e] = p.S0 != nullptr ? p.S0[sbase + (size_t)(Op::row4(t, g4) + e) * Dv] : 0.f;
+    for (int t = 0; t < CT; ++t)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) S[t][e] = p.S0[sbase + (size_t)(Op::row4(t, g4) + e) * Dv];
+  }
 
   if (sp.nch > 0) copy(0, lds);
+  __builtin_amdgcn_s_waitcnt(0);  // the first chunk's copies have no stores behind them
 #pragma unroll 1
   for (int n = 0; n < sp.nch; ++n) {
     char* buf = lds + (n & 1) * L::BYTES;
-    // this wave's copies of chunk n have landed; after the barrier everybody's
-    // have, and everybody is done with the other buffer
-    __builtin_amdgcn_s_waitcnt(0);
+    // this wave's copies of chunk n have landed (the only vector memory operations
+    // it issued after them are the stores of chunk n - 1: they may stay in flight); after the barrier everybody's have, and everybody is done with
+    // the other buffer
+    wait_vmcnt<NSTORE>();
     lds_barrier();
-    if (n + 1 < sp.nch) copy(n + 1, lds + ((n + 1) & 1) * L::BYTES);
 
+    // bytes of the chunk's rows of o, Y: what lies behind belongs to others
+    const unsigned chunk_bytes = (unsigned)((sp.Tq - n * C < C ? sp.Tq - n * C : C) * (int)HD * ES);
     const IO* iK = reinterpret_cast<const IO*>(buf + L::K);
     const IO* iV = reinterpret_cast<const IO*>(buf + L::V);
     const IO* iT = reinterpret_cast<const IO*>(buf + L::T);
@@ -95,99 +122,150 @@ __global__ __launch_bounds__(64 * WV) void kda_gdr_walk_kernel(GdrWalkParams p, 
     const IO* iP = reinterpret_cast<const IO*>(buf + L::P);
     const float* sc = reinterpret_cast<const float*>(buf + L::SC);
 
+    // The reads of each product are issued one group of products ahead; the fences
+    // keep the compiler from pulling a read and its use together, where every use
+    // would wait out the whole LDS latency.
+    constexpr int HT = TL / 2;  // token tiles of a group
+    auto rows = [&](Frag (&f)[HT][NUK], const IO* img, int t0) {
+#pragma unroll
+      for (int t = 0; t < HT; ++t)
+#pragma unroll
+        for (int u = 0; u < NUK; ++u) f[t][u] = g_row<IO, DK>(img, Op::perm(t0 + t, r), u, g4);
+    };
+    f32x4 V[TL];
+    Frag ka[HT][NUK], kc[HT][NUK];
+    rows(ka, iK, 0);
+#pragma unroll
+    for (int t = 0; t < TL; ++t) V[t] = g_acc<VB>(iV, t, 16 * wave, r, g4);  // before the copies are issued
+    __builtin_amdgcn_sched_barrier(0);
+    if (n + 1 < sp.nch) copy(n + 1, lds + ((n + 1) & 1) * L::BYTES);
+    __builtin_amdgcn_sched_barrier(0);  // the stores counted above come after the copies
+
     if constexpr (CK) {
       // the state at the chunk's start, for the gradients
-      IO* ck = static_cast<IO*>(p.ckpt) + (sp.rec0 + n * sp.rstride) * (size_t)DK * Dv +
-               (size_t)(v0 / 16) * DK * 16 + r;
+      const BufRes to = make_buf(static_cast<IO*>(p.ckpt) + (sp.rec0 + n * sp.rstride) * (size_t)DK * Dv,
+                                 (unsigned)(DK * Dv * ES));
 #pragma unroll
       for (int t = 0; t < CT; ++t)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) ck[(Op::row4(t, g4) + e) * 16] = from_f32<IO>(S[t][e]);
+        store_tile(to, Op::row4(t, g4), 16 * ES, v0 * DK * ES, S[t], r, IO{});
     }
 
-    // ---- X = V - cx (K S)
+    // ---- X = V - cx (K S);  O^T = co (S^T Q^T)
     Terms<IO, 2> s2[NUK];
 #pragma unroll
     for (int u = 0; u < NUK; ++u) s2[u].set(&S[TPU * u]);
-    f32x4 X[TL];
+    f32x4 X[TL], O[TL];
+    auto k_s = [&](const Frag (&f)[HT][NUK], int t0) {
 #pragma unroll
-    for (int t = 0; t < TL; ++t) {
-      f32x4 acc = {0.f, 0.f, 0.f, 0.f};
+      for (int t = 0; t < HT; ++t) X[t0 + t] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-      for (int u = 0; u < NUK; ++u) {
-        const Frag fk[1] = {g_row<IO, DK>(iK, Op::perm(t, r), u, g4)};
-        gmma_terms<1>(acc, fk, s2[u]);
+      for (int u = 0; u < NUK; ++u)
+#pragma unroll
+        for (int i = 0; i < s2[u].N; ++i)
+#pragma unroll
+          for (int t = 0; t < HT; ++t) gmma(X[t0 + t], f[t][u], s2[u].t[i]);
+    };
+    auto s_q = [&](const Frag (&f)[HT][NUK], int t0) {
+#pragma unroll
+      for (int t = 0; t < HT; ++t) O[t0 + t] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int u = 0; u < NUK; ++u)
+#pragma unroll
+        for (int i = 0; i < s2[u].N; ++i)
+#pragma unroll
+          for (int t = 0; t < HT; ++t) gmma(O[t0 + t], s2[u].t[i], f[t][u]);
+#pragma unroll
+      for (int t = 0; t < HT; ++t) {
+        const float co = sc[2 * C + Op::perm(t0 + t, r)];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) O[t0 + t][e] *= co;
       }
-      const f32x4 cx = *reinterpret_cast<const f32x4*>(sc + Op::row4(t, g4));
-      const f32x4 v = g_acc<VB>(iV, t, 16 * wave, r, g4);
+    };
+    auto x_of = [&](int t0) {
 #pragma unroll
-      for (int e = 0; e < 4; ++e) X[t][e] = fmaf(-cx[e], acc[e], v[e]);
-    }
-    // ---- O^T = co (S^T Q^T)
-    f32x4 O[TL];
-    if constexpr (OUT) {
+      for (int t = t0; t < t0 + HT; ++t) {
+        const f32x4 cx = *reinterpret_cast<const f32x4*>(sc + Op::row4(t, g4));
 #pragma unroll
-      for (int t = 0; t < TL; ++t) {
-        O[t] = f32x4{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-        for (int u = 0; u < NUK; ++u) {
-          const Frag fq = g_row<IO, DK>(iQ, Op::perm(t, r), u, g4);
-#pragma unroll
-          for (int i = 0; i < s2[u].N; ++i) gmma(O[t], s2[u].t[i], fq);
-        }
-        const float co = sc[2 * C + Op::perm(t, r)];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) O[t][e] *= co;
+        for (int e = 0; e < 4; ++e) X[t][e] = fmaf(-cx[e], X[t][e], V[t][e]);
       }
-    }
-    // ---- Y = Tm X (lower triangle of units)
-    Terms<IO, 3> x3[NUC];
-#pragma unroll
-    for (int u = 0; u < NUC; ++u) x3[u].set(&X[TPU * u]);
-    f32x4 Y[TL];
-#pragma unroll
-    for (int t = 0; t < TL; ++t) {
-      Y[t] = f32x4{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-      for (int u = 0; u <= t / TPU; ++u) {
-        Frag ft[TT];
-#pragma unroll
-        for (int i = 0; i < TT; ++i) ft[i] = g_row<IO, C>(iT + i * C * C, Op::perm(t, r), u, g4);
-        gmma_terms<TT>(Y[t], ft, x3[u]);
-      }
-    }
-    if constexpr (CK) {
+    };
+    // the lower triangle of units of Tm (and P) by token tile
+    constexpr int NF = NUC * (NUC + 1) / 2 * TPU;  // (tile, unit) pairs
+    Frag fT[NF][TT], fP[NF];
+    auto tri = [&]() {
+      int i = 0;
 #pragma unroll
       for (int t = 0; t < TL; ++t)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const int tt = n * C + Op::row4(t, g4) + e;
-          if (tt < sp.Tq)
-            static_cast<IO*>(p.y)[(size_t)(sp.tok0 + tt) * HD + (size_t)h * Dv + v0 + r] =
-                from_f32<IO>(Y[t][e]);
+        for (int u = 0; u <= t / TPU; ++u, ++i) {
+#pragma unroll
+          for (int k = 0; k < TT; ++k) fT[i][k] = g_row<IO, C>(iT + k * C * C, Op::perm(t, r), u, g4);
+          if constexpr (OUT) fP[i] = g_row<IO, C>(iP, Op::perm(t, r), u, g4);
         }
+    };
+    Terms<IO, 3> x3[NUC];
+    rows(kc, iK, HT);
+    __builtin_amdgcn_sched_barrier(0);
+    k_s(ka, 0);
+    if constexpr (OUT) rows(ka, iQ, 0);
+    __builtin_amdgcn_sched_barrier(0);
+    k_s(kc, HT);
+    if constexpr (OUT) {
+      rows(kc, iQ, HT);
+      __builtin_amdgcn_sched_barrier(0);
+      x_of(0);
+      s_q(ka, 0);
+      tri();
+      __builtin_amdgcn_sched_barrier(0);
+      x_of(HT);
+#pragma unroll
+      for (int u = 0; u < NUC; ++u) x3[u].set(&X[TPU * u]);
+      s_q(kc, HT);
+    } else {
+      tri();
+      __builtin_amdgcn_sched_barrier(0);
+      x_of(0);
+      x_of(HT);
+#pragma unroll
+      for (int u = 0; u < NUC; ++u) x3[u].set(&X[TPU * u]);
+    }
+    // ---- Y = Tm X
+    f32x4 Y[TL];
+    {
+      int i = 0;
+#pragma unroll
+      for (int t = 0; t < TL; ++t) {
+        Y[t] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int u = 0; u <= t / TPU; ++u, ++i) gmma_terms<TT>(Y[t], fT[i], x3[u]);
+      }
+    }
+    if constexpr (CK) {
+      const BufRes to = make_buf(static_cast<IO*>(p.y) + (size_t)(sp.tok0 + n * C) * HD, chunk_bytes);
+#pragma unroll
+      for (int t = 0; t < TL; ++t)
+        store_tile(to, Op::row4(t, g4), (int)HD * ES, (h * Dv + v0) * ES, Y[t], r, IO{});
     }
     // ---- O^T += Y^T P^T
     if constexpr (OUT) {
+      const BufRes ob = make_buf(static_cast<IO*>(p.o) + (size_t)(sp.tok0 + n * C) * HD, chunk_bytes);
       Terms<IO, 2> y2[NUC];
 #pragma unroll
       for (int u = 0; u < NUC; ++u) y2[u].set(&Y[TPU * u]);
+      int i = 0;
 #pragma unroll
       for (int t = 0; t < TL; ++t) {
 #pragma unroll
-        for (int u = 0; u <= t / TPU; ++u) {
-          const Frag fp = g_row<IO, C>(iP, Op::perm(t, r), u, g4);
+        for (int u = 0; u <= t / TPU; ++u, ++i)
 #pragma unroll
-          for (int i = 0; i < y2[u].N; ++i) gmma(O[t], y2[u].t[i], fp);
-        }
-        const int tt = n * C + Op::perm(t, r);
-        if (tt < sp.Tq)
-          store4(static_cast<IO*>(p.o) + (size_t)(sp.tok0 + tt) * HD + (size_t)h * Dv + v0 + 4 * g4,
-                 O[t][0], O[t][1], O[t][2], O[t][3]);
+          for (int k = 0; k < y2[u].N; ++k) gmma(O[t], y2[u].t[k], fP[i]);
       }
+#pragma unroll
+      for (int t = 0; t < TL; ++t)
+        store_four(ob, Op::perm(t, r) * (int)HD * ES + (h * Dv + v0 + 4 * g4) * ES, O[t], IO{});
     }
     // ---- S = gamma_C S + K^T (cy Y)
-    const float lamC = expf(sc[5 * C + C - 1] + sc[6 * C + C - 1]);
+    const float lamC = exp2_fast(sc[5 * C + C - 1] + sc[6 * C + C - 1]);
 #pragma unroll
     for (int t = 0; t < TL; ++t) {
       const f32x4 cy = *reinterpret_cast<const f32x4*>(sc + C + Op::row4(t, g4));
@@ -198,14 +276,20 @@ __global__ __launch_bounds__(64 * WV) void kda_gdr_walk_kernel(GdrWalkParams p, 
 #pragma unroll
     for (int u = 0; u < NUC; ++u) y3[u].set(&Y[TPU * u]);
 #pragma unroll
-    for (int t = 0; t < CT; ++t) {
+    for (int t = 0; t < CT; ++t)
 #pragma unroll
       for (int e = 0; e < 4; ++e) S[t][e] *= lamC;
 #pragma unroll
-      for (int u = 0; u < NUC; ++u) {
-        const Frag fk[1] = {g_colp<DK>(iK, u, t, r, g4)};
-        gmma_terms<1>(S[t], fk, y3[u]);
-      }
+    for (int jj = 0; jj < CT / 2; ++jj) {
+      Frag f0[NUC], f1[NUC];
+      g_colp_pair<DK>(iK, jj, r, g4, f0, f1);
+#pragma unroll
+      for (int u = 0; u < NUC; ++u)
+#pragma unroll
+        for (int k = 0; k < y3[u].N; ++k) {
+          gmma(S[2 * jj], f0[u], y3[u].t[k]);
+          gmma(S[2 * jj + 1], f1[u], y3[u].t[k]);
+        }
     }
   }
   if (p.S_T != nullptr) {

@@ -5,6 +5,7 @@
 // that no page is both read and written: a fork reads pages in use and writes free
 // ones, a compaction reads pages behind the first n_used and writes free ones
 // before them, a copy leaves such pairs out.
+#include "kda_device.h"
 #include "kda_gdr.h"
 #include "kda_launch.h"
 
@@ -13,7 +14,6 @@ namespace kda {
 namespace {
 
 constexpr int PT = 1024;
-typedef unsigned u32x4 __attribute__((ext_vector_type(4)));
 
 // Exclusive running sum over the workgroup's PT threads; *total gets the sum.
 __device__ __forceinline__ int block_excl(int x, int* red, int* total) {
