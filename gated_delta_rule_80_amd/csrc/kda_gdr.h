@@ -24,26 +24,31 @@ namespace kda {
 // matrices fit LDS together (bf16 64, float32 32).
 constexpr int gdr_chunk(bool fp32) { return fp32 ? 32 : 64; }
 
-// One record per (sequence, value head, chunk), element type E:
-//   Tm   [TT][C][C]  row-major, TT terms: bf16 keeps Tm as hi + lo (16 bits of
+// One record per (sequence, value head, chunk), element type E.  A matrix is kept as
+// the matrix-core operands the walks read, in their order: one fragment of 64 lanes x
+// 16 bytes per (token tile, contraction unit) of its triangle (kda_gdr_device.h), so
+// that a workgroup copies it to LDS as it stands and a lane's reads are consecutive.
+//   Tm   [6 | 3][TT]  fragments in TT terms: bf16 keeps Tm as hi + lo (16 bits of
 //                    mantissa), float32 as it is
 //   sc   [8][C]      float32, per token: cx = gamma rk, cy = b lambda rk,
 //                    co = scale gamma rq, rk, rq, G in log2 units (high part, low
 //                    part), b; rows behind the sequence's end hold zeros in cx,
 //                    cy, co, rk, rq, b
-//   P    [C][C]      forward: one term (its products end in the output)
+//   P    [6 | 3]     forward: one term (its products end in the output)
 // or, for the backward (whose dS0 leaves in float32),
-//   P^T, Tm^T [TT][C][C]  the transposes, rows as the reverse walk reads them
+//   P^T, Tm^T [6 | 3][TT]
 // where rk, rq are 1 / norm (1 without the normalisation).
 struct GdrRecord {
   size_t t, sc, p, tt;  // byte offsets
   size_t bytes;         // 256-byte multiple
 };
 constexpr int kGdrScalars = 8;
+// fragments of a triangle: bf16 4 token tiles x 2 units of 2 tiles, float32 2 x 2
+constexpr int gdr_frags(bool fp32) { return fp32 ? 3 : 6; }
 
 constexpr GdrRecord gdr_record(bool fp32, bool bwd) {
-  const size_t C = (size_t)gdr_chunk(fp32), es = fp32 ? 4 : 2, terms = fp32 ? 1 : 2;
-  const size_t mat = C * C * es;
+  const size_t C = (size_t)gdr_chunk(fp32), terms = fp32 ? 1 : 2;
+  const size_t mat = (size_t)gdr_frags(fp32) * 1024;
   GdrRecord r{};
   r.t = 0;
   r.sc = terms * mat;
@@ -62,6 +67,9 @@ struct GdrShape {
   long qs, ks, vs;   // elements between tokens of q, k, v
   SeqTables seqs;    // bounds NULL: equal lengths
 };
+
+// Waves (of 16 value columns each) in a walk's workgroup.
+constexpr int gdr_walk_waves(int Dv, bool fp32) { return Dv >= 128 ? (fp32 ? 4 : 8) : Dv / 16; }
 
 struct GdrPrepParams {
   GdrShape s;

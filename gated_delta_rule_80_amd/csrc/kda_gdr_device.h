@@ -214,16 +214,28 @@ template <int NT> struct Terms<float, NT> {
   __device__ __forceinline__ void set(const f32x4* tiles) { t[0] = tiles[0]; }
 };
 
-// acc += A B for an operand given in AT terms and one in BT terms: products of
-// terms i, j with i + j < max(AT, BT) (the others are below the last kept term).
-template <int AT, typename F, typename TB>
-__device__ __forceinline__ void gmma_terms(f32x4& acc, const F (&a)[AT], const TB& b) {
-  constexpr int LIM = AT > TB::N ? AT : TB::N;
-#pragma unroll
-  for (int i = 0; i < AT; ++i)
-#pragma unroll
-    for (int j = 0; j < TB::N; ++j)
-      if (i + j < LIM) gmma(acc, a[i], b.t[j]);
+// Position of (token tile t, unit u) in the list of a triangle's fragments, tile by
+// tile: units u <= t / TPU of each tile (lower), or u >= t / TPU (the transpose).
+template <int TPU, int NU, bool UPPER> __host__ __device__ constexpr int tri_at(int t, int u) {
+  int i = 0;
+  for (int s = 0; s < NU * TPU; ++s)
+    if (s < t) i += UPPER ? NU - s / TPU : s / TPU + 1;
+  return i + (UPPER ? u - t / TPU : u);
+}
+// Offset in elements of element (i, j) of the matrix (j's fragment slot may be
+// written in parts), term k of `terms`.
+template <typename E, int NU, bool UPPER>
+__device__ __forceinline__ int tri_slot(int i, int j, int k, int terms) {
+  constexpr int KU = GOp<E>::KU, TPU = GOp<E>::TPU;
+  const int t = KU == 32 ? 2 * (i >> 5) + ((i >> 2) & 1) : i >> 4;
+  const int r = KU == 32 ? 4 * ((i >> 3) & 3) + (i & 3) : i & 15;
+  const int u = j / KU, g = j % KU / (KU / 4), e = j % (KU / 4);
+  return ((tri_at<TPU, NU, UPPER>(t, u) * terms + k) * 64 + r + 16 * g) * (KU / 4) + e;
+}
+// This lane's fragment f of a list in LDS.
+template <typename E>
+__device__ __forceinline__ typename GOp<E>::Frag g_frag(const E* list, int f, int lane) {
+  return *reinterpret_cast<const typename GOp<E>::Frag*>(list + (f * 64 + lane) * (16 / (int)sizeof(E)));
 }
 
 // 2^x by the hardware instruction (1 ulp; results below 2^-126 are 0, and so is the

@@ -43,6 +43,13 @@ __device__ __forceinline__ float frag_dot(const f32x4& a, const f32x4& b, float 
   return s;
 }
 
+// acc += A B, B in all its terms
+template <typename F, typename TB>
+__device__ __forceinline__ void gmma_all(f32x4& acc, const F& a, const TB& b) {
+#pragma unroll
+  for (int k = 0; k < TB::N; ++k) gmma(acc, a, b.t[k]);
+}
+
 // sum over the 4 lane groups (lanes of one r)
 __device__ __forceinline__ float sum_groups(float x) {
   x += __shfl_xor(x, 16, 64);
@@ -214,11 +221,11 @@ __global__ __launch_bounds__(256) void kda_gdr_grad_kernel(GdrGradParams p) {
       }
 #pragma unroll
       for (int c = 0; c < CW; ++c) {
-        const Frag fk[1] = {g_col<DK>(iK, u, c0 + 16 * c, r, g4)};
+        const Frag fk = g_col<DK>(iK, u, c0 + 16 * c, r, g4);
 #pragma unroll
         for (int t = 0; t < TW; ++t) {
-          gmma_terms<1>(aq[c][t], fk, e1[t]);
-          gmma_terms<1>(ae[c][t], fk, e2[t]);
+          gmma_all(aq[c][t], fk, e1[t]);
+          gmma_all(ae[c][t], fk, e2[t]);
         }
       }
     }
@@ -262,12 +269,12 @@ __global__ __launch_bounds__(256) void kda_gdr_grad_kernel(GdrGradParams p) {
       }
 #pragma unroll
       for (int c = 0; c < CW; ++c) {
-        const Frag fq[1] = {g_col<DK>(iQ, u, c0 + 16 * c, r, g4)};
-        const Frag fk[1] = {g_col<DK>(iK, u, c0 + 16 * c, r, g4)};
+        const Frag fq = g_col<DK>(iQ, u, c0 + 16 * c, r, g4);
+        const Frag fk = g_col<DK>(iK, u, c0 + 16 * c, r, g4);
 #pragma unroll
         for (int t = 0; t < TW; ++t) {
-          gmma_terms<1>(aw[c][t], fq, e1[t]);
-          gmma_terms<1>(aw[c][t], fk, e2[t]);
+          gmma_all(aw[c][t], fq, e1[t]);
+          gmma_all(aw[c][t], fk, e2[t]);
         }
       }
     }

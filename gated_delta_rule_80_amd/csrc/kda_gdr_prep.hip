@@ -19,6 +19,7 @@ __global__ __launch_bounds__(256) void kda_gdr_prep_kernel(GdrPrepParams p) {
   constexpr bool F32 = sizeof(IO) == 4;
   constexpr int C = gdr_chunk(F32);
   constexpr int NTL = C / 16;                // tiles per side
+  constexpr int TPU = GOp<IO>::TPU, NUC = NTL / TPU, TT = F32 ? 1 : 2;
   constexpr GdrRecord R = gdr_record(F32, BWD);
   using I = GImg<IO, DK>;
   using Frag = typename GOp<IO>::Frag;
@@ -121,8 +122,9 @@ __global__ __launch_bounds__(256) void kda_gdr_prep_kernel(GdrPrepParams p) {
 #pragma unroll
     for (int tj = 0; tj < NTL; ++tj) {
       if (tj > wave) {
-        // the upper half of a diagonal 32 x 32 block is read as part of its rows
-        if (!BWD && (tj >> 1) == (wave >> 1)) store4(recP + i * C + 16 * tj + 4 * g4, 0.f, 0.f, 0.f, 0.f);
+        // the upper half of a diagonal unit is part of its rows' fragments
+        if (!BWD && tj / TPU == wave / TPU)
+          store4(recP + tri_slot<IO, NUC, false>(i, 16 * tj + 4 * g4, 0, 1), 0.f, 0.f, 0.f, 0.f);
         continue;
       }
       f32x4 kk = {0.f, 0.f, 0.f, 0.f}, qk = {0.f, 0.f, 0.f, 0.f};
@@ -143,7 +145,7 @@ __global__ __launch_bounds__(256) void kda_gdr_prep_kernel(GdrPrepParams p) {
         pv[e] = i >= j + e ? d * si * qk[e] : 0.f;
       }
       *reinterpret_cast<f32x4*>(&As[i * LA + j]) = av;
-      if constexpr (!BWD) store4(recP + i * C + j, pv[0], pv[1], pv[2], pv[3]);
+      if constexpr (!BWD) store4(recP + tri_slot<IO, NUC, false>(i, j, 0, 1), pv[0], pv[1], pv[2], pv[3]);
     }
     if constexpr (BWD) {
       // P^T, rows j = 16 wave + r: lanes hold i = 16 ti + 4 g4 ..
@@ -151,12 +153,11 @@ __global__ __launch_bounds__(256) void kda_gdr_prep_kernel(GdrPrepParams p) {
       const float bj = bi * ri;
 #pragma unroll
       for (int ti = 0; ti < NTL; ++ti) {
-        IO* to = recP + j * C + 16 * ti + 4 * g4;
         if (ti < wave) {
-          if ((ti >> 1) == (wave >> 1)) {
-            store4(to, 0.f, 0.f, 0.f, 0.f);
-            if constexpr (!F32) store4(to + C * C, 0.f, 0.f, 0.f, 0.f);
-          }
+          if (ti / TPU == wave / TPU)
+#pragma unroll
+            for (int k = 0; k < TT; ++k)
+              store4(recP + tri_slot<IO, NUC, true>(j, 16 * ti + 4 * g4, k, TT), 0.f, 0.f, 0.f, 0.f);
           continue;
         }
         f32x4 qk = {0.f, 0.f, 0.f, 0.f};
@@ -172,8 +173,8 @@ __global__ __launch_bounds__(256) void kda_gdr_prep_kernel(GdrPrepParams p) {
           pv[e] = i4 + e >= j ? d * (s_i[e] * p.scale) * qk[e] : 0.f;
           lo[e] = pv[e] - to_f32(from_f32<IO>(pv[e]));
         }
-        store4(to, pv[0], pv[1], pv[2], pv[3]);
-        if constexpr (!F32) store4(to + C * C, lo[0], lo[1], lo[2], lo[3]);
+        store4(recP + tri_slot<IO, NUC, true>(j, i4, 0, TT), pv[0], pv[1], pv[2], pv[3]);
+        if constexpr (!F32) store4(recP + tri_slot<IO, NUC, true>(j, i4, 1, TT), lo[0], lo[1], lo[2], lo[3]);
       }
     }
   }
@@ -222,28 +223,32 @@ __global__ __launch_bounds__(256) void kda_gdr_prep_kernel(GdrPrepParams p) {
     }
     __syncthreads();
   }
-  // ---- Tm (for the backward also Tm^T) and the scalars to the record
+  // ---- Tm (for the backward also Tm^T) and the scalars to the record, a fragment a
+  // wave at a time
 #pragma unroll
   for (int n = 0; n < (BWD ? 2 : 1); ++n) {
     IO* to = reinterpret_cast<IO*>(rec + (n ? R.tt : R.t));
-    for (int idx = tid; idx < C * C / EPC; idx += 256) {
-      // n = 1: consecutive threads take consecutive columns of Tm, so that their
-      // reads down a column fall into different banks
-      const int i = n ? idx % C : idx / (C / EPC), j = (n ? idx / C : idx % (C / EPC)) * EPC;
-      const bool in = n ? (j >> 4) >= (i >> 4) : (j >> 4) <= (i >> 4);
-      float x[EPC];
+    int f = 0;
 #pragma unroll
-      for (int e = 0; e < EPC; ++e) x[e] = in ? (n ? Ts[(j + e) * LA + i] : Ts[i * LA + j + e]) : 0.f;
-      if constexpr (F32) {
-        *reinterpret_cast<f32x4*>(to + i * C + j) = f32x4{x[0], x[1], x[2], x[3]};
-      } else {
-        float lo[8];
+    for (int t = 0; t < NTL; ++t)
 #pragma unroll
-        for (int e = 0; e < EPC; ++e) lo[e] = x[e] - (float)(__bf16)x[e];
-        store8(to + i * C + j, x);
-        store8(to + C * C + i * C + j, lo);
+      for (int u = n ? t / TPU : 0; u < (n ? NUC : t / TPU + 1); ++u, ++f) {
+        if (((f + n) & 3) != wave) continue;
+        const int i = GOp<IO>::perm(t, r), j = GOp<IO>::KU * u + (GOp<IO>::KU / 4) * g4;
+        const bool in = n ? (j >> 4) >= (i >> 4) : (j >> 4) <= (i >> 4);
+        float x[EPC];
+#pragma unroll
+        for (int e = 0; e < EPC; ++e) x[e] = in ? (n ? Ts[(j + e) * LA + i] : Ts[i * LA + j + e]) : 0.f;
+        if constexpr (F32) {
+          *reinterpret_cast<f32x4*>(to + (f * 64 + lane) * 4) = f32x4{x[0], x[1], x[2], x[3]};
+        } else {
+          float lo[8];
+#pragma unroll
+          for (int e = 0; e < EPC; ++e) lo[e] = x[e] - (float)(__bf16)x[e];
+          store8(to + (2 * f * 64 + lane) * 8, x);
+          store8(to + ((2 * f + 1) * 64 + lane) * 8, lo);
+        }
       }
-    }
   }
   float* recS = reinterpret_cast<float*>(rec + R.sc);
   for (int idx = tid; idx < kGdrScalars * C; idx += 256) recS[idx] = sc[idx / C][idx % C];

@@ -19,11 +19,12 @@ struct GdrReverseLds {
   static constexpr int TT = F32 ? 1 : 2;  // terms of Tm and of P
   static constexpr int K = 0;
   static constexpr int Q = K + C * DK * ES;
-  static constexpr int T = Q + C * DK * ES;
-  static constexpr int P = T + TT * C * C * ES;
-  static constexpr int DO = P + TT * C * C * ES;
-  static constexpr int SC = DO + C * VB * ES;
-  static constexpr int BYTES = SC + kGdrScalars * C * 4;
+  static constexpr int TB = TT * gdr_frags(F32) * 1024;
+  static constexpr int SC = Q + C * DK * ES;  // sc, P^T, Tm^T as in the record
+  static constexpr int P = SC + kGdrScalars * C * 4;
+  static constexpr int T = P + TB;
+  static constexpr int DO = T + TB;
+  static constexpr int BYTES = DO + C * VB * ES;
 };
 
 template <int DK, int WV, typename IO>
@@ -54,11 +55,9 @@ __global__ __launch_bounds__(64 * WV) void kda_gdr_reverse_kernel(GdrReversePara
 
   GdrCopy<NT, C, DK, IO> ck, cq;
   GdrCopy<NT, C, VB, IO> co;
-  GdrCopy<NT, TT * C, C, IO> ct;
   ck.init(p.s.ks);
   cq.init(p.s.qs);
   co.init(HD);
-  ct.init(C);
   auto copy = [&](int n, char* buf) {
     const int last = sp.Tq - n * C - 1;
     const long t0 = (long)n * C;
@@ -75,9 +74,8 @@ __global__ __launch_bounds__(64 * WV) void kda_gdr_reverse_kernel(GdrReversePara
       cq.part(buf + L::Q, pq, p.s.qs, last, wave);
       co.part(buf + L::DO, po, HD, last, wave);
     }
-    ct.whole(buf + L::T, reinterpret_cast<const IO*>(rec + R.tt), wave);
-    ct.whole(buf + L::P, reinterpret_cast<const IO*>(rec + R.p), wave);
-    gdr_copy_flat<NT, kGdrScalars * C * 4>(buf + L::SC, rec + R.sc, wave);
+    static_assert(R.p == R.sc + kGdrScalars * C * 4 && R.tt == R.p + L::TB, "one run of the record");
+    gdr_copy_flat<NT, kGdrScalars * C * 4 + 2 * L::TB>(buf + L::SC, rec + R.sc, wave);
   };
 
   f32x4 dS[CT];
@@ -156,48 +154,44 @@ __global__ __launch_bounds__(64 * WV) void kda_gdr_reverse_kernel(GdrReversePara
       }
     };
     // the upper triangles of units of P^T and Tm^T
-    constexpr int NF = NUC * (NUC + 1) / 2 * TPU;
+    constexpr int NF = gdr_frags(F32);
     Frag fT[NF][TT], fP[NF][TT];
-    auto tri = [&](Frag (&f)[NF][TT], const IO* img) {
-      int i = 0;
+    auto tri = [&](Frag (&f)[NF][TT], const IO* list) {
 #pragma unroll
-      for (int t = 0; t < TL; ++t)
+      for (int i = 0; i < NF; ++i)
 #pragma unroll
-        for (int u = t / TPU; u < NUC; ++u, ++i)
-#pragma unroll
-          for (int k = 0; k < TT; ++k) f[i][k] = g_row<IO, C>(img + k * C * C, Op::perm(t, r), u, g4);
+        for (int k = 0; k < TT; ++k) f[i][k] = g_frag(list, i * TT + k, lane);
     };
     rows(kc, HT);
-    __builtin_amdgcn_sched_barrier(0);
+    if constexpr (WV <= 4) __builtin_amdgcn_sched_barrier(0);
     k_s(ka, 0);
     tri(fP, iP);
-    __builtin_amdgcn_sched_barrier(0);
+    if constexpr (WV <= 4) __builtin_amdgcn_sched_barrier(0);
     k_s(kc, HT);
     tri(fT, iT);
-    __builtin_amdgcn_sched_barrier(0);
-    {
-      int i = 0;
+    if constexpr (WV <= 4) __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-      for (int t = 0; t < TL; ++t)
+    for (int u = 0; u < NUC; ++u)
 #pragma unroll
-        for (int u = t / TPU; u < NUC; ++u, ++i)
+      for (int k = 0; k < TT; ++k)
 #pragma unroll
-          for (int k = 0; k < TT; ++k) gmma(dY[t], fP[i][k], o1[u].t[0]);
-    }
+        for (int t = 0; t < TPU * (u + 1); ++t) gmma(dY[t], fP[tri_at<TPU, NUC, true>(t, u)][k], o1[u].t[0]);
     // ---- dX = Tm^T dY
     Terms<IO, 3> y3[NUC];
 #pragma unroll
     for (int u = 0; u < NUC; ++u) y3[u].set(&dY[TPU * u]);
     f32x4 dX[TL];
-    {
-      int i = 0;
 #pragma unroll
-      for (int t = 0; t < TL; ++t) {
-        dX[t] = f32x4{0.f, 0.f, 0.f, 0.f};
+    for (int t = 0; t < TL; ++t) dX[t] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-        for (int u = t / TPU; u < NUC; ++u, ++i) gmma_terms<TT>(dX[t], fT[i], y3[u]);
-      }
-    }
+    for (int u = 0; u < NUC; ++u)
+#pragma unroll
+      for (int k = 0; k < TT; ++k)
+#pragma unroll
+        for (int j = 0; j < y3[u].N; ++j)
+          if (k + j < y3[u].N)  // the products below the third term are left out
+#pragma unroll
+            for (int t = 0; t < TPU * (u + 1); ++t) gmma(dX[t], fT[tri_at<TPU, NUC, true>(t, u)][k], y3[u].t[j]);
     // ---- dS = gamma_C dS + Q^T (co dO) - K^T (cx dX); the first while dX forms
 #pragma unroll
     for (int t = 0; t < TL; ++t) {
@@ -258,8 +252,13 @@ __global__ __launch_bounds__(64 * WV) void kda_gdr_reverse_kernel(GdrReversePara
 
 template <int DK, typename IO>
 static hipError_t launch_reverse_w(const GdrReverseParams& p, int Dv, hipStream_t st) {
-  const int wv = Dv % 64 == 0 ? 4 : 2;
+  const int wv = gdr_walk_waves(Dv, sizeof(IO) == 4);
   const unsigned grid = (unsigned)((size_t)p.s.NS * p.s.Hv * (Dv / (16 * wv)));
+  if constexpr (sizeof(IO) == 2)
+    if (wv == 8) {
+      hipLaunchKernelGGL((kda_gdr_reverse_kernel<DK, 8, IO>), dim3(grid), dim3(512), 0, st, p, Dv);
+      return hipGetLastError();
+    }
   if (wv == 4)
     hipLaunchKernelGGL((kda_gdr_reverse_kernel<DK, 4, IO>), dim3(grid), dim3(256), 0, st, p, Dv);
   else

@@ -24,10 +24,11 @@ struct GdrWalkLds {
   static constexpr int K = 0;
   static constexpr int V = K + C * DK * ES;
   static constexpr int T = V + C * VB * ES;
-  static constexpr int SC = T + TT * C * C * ES;
+  static constexpr int TB = TT * gdr_frags(F32) * 1024, PB = gdr_frags(F32) * 1024;
+  static constexpr int SC = T + TB;
   static constexpr int Q = SC + kGdrScalars * C * 4;
   static constexpr int P = Q + (OUT ? C * DK * ES : 0);
-  static constexpr int BYTES = P + (OUT ? C * C * ES : 0);
+  static constexpr int BYTES = P + (OUT ? PB : 0);
 };
 
 template <int DK, int WV, typename IO, bool OUT, bool CK>
@@ -60,15 +61,9 @@ __global__ __launch_bounds__(64 * WV) void kda_gdr_walk_kernel(GdrWalkParams p, 
 
   GdrCopy<NT, C, DK, IO> ck, cq;
   GdrCopy<NT, C, VB, IO> cv;
-  GdrCopy<NT, TT * C, C, IO> ct;
-  GdrCopy<NT, C, C, IO> cp;
   ck.init(p.s.ks);
   cv.init(p.s.vs);
-  ct.init(C);
-  if constexpr (OUT) {
-    cq.init(p.s.qs);
-    cp.init(C);
-  }
+  if constexpr (OUT) cq.init(p.s.qs);
   auto copy = [&](int n, char* buf) {
     const int last = sp.Tq - n * C - 1;  // >= 0: the chunk exists
     const long t0 = (long)n * C;
@@ -85,9 +80,9 @@ __global__ __launch_bounds__(64 * WV) void kda_gdr_walk_kernel(GdrWalkParams p, 
       cv.part(buf + L::V, pv, p.s.vs, last, wave);
       if constexpr (OUT) cq.part(buf + L::Q, pq, p.s.qs, last, wave);
     }
-    ct.whole(buf + L::T, reinterpret_cast<const IO*>(rec + R.t), wave);
-    if constexpr (OUT) cp.whole(buf + L::P, reinterpret_cast<const IO*>(rec + R.p), wave);
-    gdr_copy_flat<NT, kGdrScalars * C * 4>(buf + L::SC, rec + R.sc, wave);
+    // Tm and the scalars follow one another in the record and in LDS
+    gdr_copy_flat<NT, L::TB + kGdrScalars * C * 4>(buf + L::T, rec + R.t, wave);
+    if constexpr (OUT) gdr_copy_flat<NT, L::PB>(buf + L::P, rec + R.p, wave);
   };
 
   // ---- initial state
@@ -190,56 +185,56 @@ __global__ __launch_bounds__(64 * WV) void kda_gdr_walk_kernel(GdrWalkParams p, 
       }
     };
     // the lower triangle of units of Tm (and P) by token tile
-    constexpr int NF = NUC * (NUC + 1) / 2 * TPU;  // (tile, unit) pairs
+    constexpr int NF = gdr_frags(F32);  // (tile, unit) pairs
     Frag fT[NF][TT], fP[NF];
     auto tri = [&]() {
-      int i = 0;
 #pragma unroll
-      for (int t = 0; t < TL; ++t)
+      for (int i = 0; i < NF; ++i) {
 #pragma unroll
-        for (int u = 0; u <= t / TPU; ++u, ++i) {
-#pragma unroll
-          for (int k = 0; k < TT; ++k) fT[i][k] = g_row<IO, C>(iT + k * C * C, Op::perm(t, r), u, g4);
-          if constexpr (OUT) fP[i] = g_row<IO, C>(iP, Op::perm(t, r), u, g4);
-        }
+        for (int k = 0; k < TT; ++k) fT[i][k] = g_frag(iT, i * TT + k, lane);
+        if constexpr (OUT) fP[i] = g_frag(iP, i, lane);
+      }
     };
     Terms<IO, 3> x3[NUC];
     rows(kc, iK, HT);
-    __builtin_amdgcn_sched_barrier(0);
+    if constexpr (WV <= 4) __builtin_amdgcn_sched_barrier(0);
     k_s(ka, 0);
     if constexpr (OUT) rows(ka, iQ, 0);
-    __builtin_amdgcn_sched_barrier(0);
+    if constexpr (WV <= 4) __builtin_amdgcn_sched_barrier(0);
     k_s(kc, HT);
     if constexpr (OUT) {
       rows(kc, iQ, HT);
-      __builtin_amdgcn_sched_barrier(0);
+      if constexpr (WV <= 4) __builtin_amdgcn_sched_barrier(0);
       x_of(0);
       s_q(ka, 0);
       tri();
-      __builtin_amdgcn_sched_barrier(0);
+      if constexpr (WV <= 4) __builtin_amdgcn_sched_barrier(0);
       x_of(HT);
 #pragma unroll
       for (int u = 0; u < NUC; ++u) x3[u].set(&X[TPU * u]);
       s_q(kc, HT);
     } else {
       tri();
-      __builtin_amdgcn_sched_barrier(0);
+      if constexpr (WV <= 4) __builtin_amdgcn_sched_barrier(0);
       x_of(0);
       x_of(HT);
 #pragma unroll
       for (int u = 0; u < NUC; ++u) x3[u].set(&X[TPU * u]);
     }
-    // ---- Y = Tm X
+    // ---- Y = Tm X, term by term over all the tiles, so that consecutive products
+    // go to different accumulators
     f32x4 Y[TL];
-    {
-      int i = 0;
 #pragma unroll
-      for (int t = 0; t < TL; ++t) {
-        Y[t] = f32x4{0.f, 0.f, 0.f, 0.f};
+    for (int t = 0; t < TL; ++t) Y[t] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-        for (int u = 0; u <= t / TPU; ++u, ++i) gmma_terms<TT>(Y[t], fT[i], x3[u]);
-      }
-    }
+    for (int u = 0; u < NUC; ++u)
+#pragma unroll
+      for (int k = 0; k < TT; ++k)
+#pragma unroll
+        for (int j = 0; j < x3[u].N; ++j)
+          if (k + j < x3[u].N)  // the products below the third term are left out
+#pragma unroll
+            for (int t = TPU * u; t < TL; ++t) gmma(Y[t], fT[tri_at<TPU, NUC, false>(t, u)][k], x3[u].t[j]);
     if constexpr (CK) {
       const BufRes to = make_buf(static_cast<IO*>(p.y) + (size_t)(sp.tok0 + n * C) * HD, chunk_bytes);
 #pragma unroll
@@ -252,14 +247,12 @@ __global__ __launch_bounds__(64 * WV) void kda_gdr_walk_kernel(GdrWalkParams p, 
       Terms<IO, 2> y2[NUC];
 #pragma unroll
       for (int u = 0; u < NUC; ++u) y2[u].set(&Y[TPU * u]);
-      int i = 0;
 #pragma unroll
-      for (int t = 0; t < TL; ++t) {
+      for (int u = 0; u < NUC; ++u)
 #pragma unroll
-        for (int u = 0; u <= t / TPU; ++u, ++i)
+        for (int k = 0; k < y2[u].N; ++k)
 #pragma unroll
-          for (int k = 0; k < y2[u].N; ++k) gmma(O[t], y2[u].t[k], fP[i]);
-      }
+          for (int t = TPU * u; t < TL; ++t) gmma(O[t], y2[u].t[k], fP[tri_at<TPU, NUC, false>(t, u)]);
 #pragma unroll
       for (int t = 0; t < TL; ++t)
         store_four(ob, Op::perm(t, r) * (int)HD * ES + (h * Dv + v0 + 4 * g4) * ES, O[t], IO{});
@@ -317,6 +310,9 @@ static hipError_t launch_walk_w(const GdrWalkParams& p, int Dv, int wv, hipStrea
   switch (wv) {
     case 2: return launch_walk_t<DK, 2, IO>(p, Dv, st);
     case 4: return launch_walk_t<DK, 4, IO>(p, Dv, st);
+    case 8:
+      if constexpr (sizeof(IO) == 2) return launch_walk_t<DK, 8, IO>(p, Dv, st);
+      break;
   }
   return hipErrorInvalidValue;
 }
@@ -332,7 +328,7 @@ static hipError_t launch_walk_d(const GdrWalkParams& p, int Dk, int Dv, int wv, 
 }
 
 hipError_t launch_gdr_walk(const GdrWalkParams& p, int Dk, int Dv, bool fp32, hipStream_t st) {
-  const int wv = Dv % 64 == 0 ? 4 : 2;
+  const int wv = gdr_walk_waves(Dv, fp32);
   return fp32 ? launch_walk_d<float>(p, Dk, Dv, wv, st) : launch_walk_d<__bf16>(p, Dk, Dv, wv, st);
 }
 
