@@ -8,7 +8,6 @@ stride between tokens.
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
 
 import torch
@@ -71,27 +70,37 @@ def declare(lib):
 
 
 # ------------------------------------------------------------------ helpers
-def _expect(t, name, shape, dtype, device):
-    if t is None:
-        return
-    if tuple(t.shape) != tuple(shape):
+# A call on a small model is a few microseconds of GPU time, so the checks below are
+# plain comparisons and only a failing one formats anything.
+def _wrong(name, t, shape, dtype, device):
+    if t.shape != shape:
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
     if t.dtype != dtype:
         raise TypeError(f"{name} is {t.dtype}, expected {dtype}")
-    if t.device != device:
-        raise ValueError(f"{name} is on {t.device}, expected {device}")
+    raise ValueError(f"{name} is on {t.device}, expected {device}")
 
 
-def _rows(t, name):
+def _dense(t, name, shape, dtype, device):
+    """Address of a contiguous tensor of this shape, type and device (None stays None)."""
+    if t is None:
+        return None
+    if t.shape != shape or t.dtype != dtype or t.device != device:
+        _wrong(name, t, shape, dtype, device)
+    if not t.is_contiguous():
+        raise ValueError(f"{name}: libkda needs contiguous tensors")
+    return t.data_ptr() or None
+
+
+def _rows(t, name, shape, dtype, device):
     """(address, elements between tokens; 0 = packed) of [B, T, H, D] or [N, H, D]."""
-    if t.numel() == 0:
-        return None, 0
+    if t.shape != shape or t.dtype != dtype or t.device != device:
+        _wrong(name, t, shape, dtype, device)
     if t.is_contiguous():
-        return t.data_ptr(), 0
-    H, D = t.shape[-2:]
-    lead, st = t.shape[:-2], t.stride()
-    if (D > 1 and st[-1] != 1) or (H > 1 and st[-2] != D):
+        return t.data_ptr() or None, 0
+    st = t.stride()
+    if (shape[-1] > 1 and st[-1] != 1) or (shape[-2] > 1 and st[-2] != shape[-1]):
         raise ValueError(f"{name}: the last two dimensions must be dense")
+    lead = shape[:-2]
     step = st[len(lead) - 1]
     if len(lead) == 2:
         if lead[1] == 1:
@@ -103,43 +112,53 @@ def _rows(t, name):
     return t.data_ptr(), step
 
 
-def _device(t):
-    """The context that makes t's device current, if it is not."""
-    if t.device.type != "cuda" or t.device.index == torch.cuda.current_device():
-        return contextlib.nullcontext()
-    return torch.cuda.device(t.device)
+def _elsewhere(t):
+    """The context that makes t's device current; None if it is."""
+    d = t.device
+    if d.type != "cuda" or d.index == torch.cuda.current_device():
+        return None
+    return torch.cuda.device(d)
 
 
-def _stream(stream, device):
-    return torch.cuda.current_stream(device) if stream is None else stream
-
-
-def _handle(stream):
+def _handle(stream, device):
+    if stream is None:
+        return torch.cuda.current_stream(device).cuda_stream
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else stream
 
 
-def _scratch(need, device, stream, own):
-    """A workspace of `need` bytes; where the call runs on another stream than the
-    one torch allocates for, torch keeps the memory until that stream is done."""
-    if own is not None or need == 0:
-        return own
-    ws = torch.empty(need, dtype=torch.uint8, device=device)
-    _used(stream, ws)
-    return ws
-
-
 def _used(stream, *tensors):
-    if isinstance(stream, torch.cuda.Stream) and stream != torch.cuda.current_stream(stream.device):
+    """Tensors made here, in a call on the caller's own stream: torch keeps their
+    memory until that stream is done with them."""
+    if isinstance(stream, torch.cuda.Stream):
         for t in tensors:
             if t is not None:
                 t.record_stream(stream)
+
+
+def _after_fill(stream, device):
+    """Has the caller's stream wait for fills made here on the current one."""
+    if isinstance(stream, torch.cuda.Stream):
+        stream.wait_stream(torch.cuda.current_stream(device))
+
+
+def _scratch(need, device, stream, own):
+    """(address, bytes) of the workspace, and what keeps it."""
+    if own is not None:
+        return (_lib._ptr(own), own.numel() * own.element_size()), own
+    if need == 0:
+        return (None, 0), None
+    ws = torch.empty(need, dtype=torch.uint8, device=device)
+    if stream is not None:
+        _used(stream, ws)
+    return (ws.data_ptr(), need), ws
 
 
 def _ws(ws):
     return (None, 0) if ws is None else (_lib._ptr(ws), ws.numel() * ws.element_size())
 
 
-def _int32(t, name, device):
+def _list(t, name, device):
+    """Address of an int32 list on the device."""
     if t.dtype != torch.int32:
         raise TypeError(f"{name} must be int32")
     if t.device != device:
@@ -151,34 +170,24 @@ def _int32(t, name, device):
 def gdr_args(q, k, v, g, beta, S0=None, o=None, S_T=None, *, scale=1.0, l2norm_qk=True, eps=1e-6,
              A_log=None, dt_bias=None, beta_logits=False, cu_seqlens=None) -> GdrArgs:
     """Fill kda_gdr_args from tensors (shapes as kda_gdr_prefill)."""
-    B, T, Hk, Dk = q.shape
-    Hv, Dv = v.shape[2:]
-    io, dev = q.dtype, q.device
-    a = GdrArgs()
-    a.io = _lib._io_of(q)
-    _expect(k, "k", (B, T, Hk, Dk), io, dev)
-    _expect(v, "v", (B, T, Hv, Dv), io, dev)
-    _expect(g, "g", (B, T, Hv), io, dev)
-    _expect(beta, "beta", (B, T, Hv), io, dev)
-    NS = B if cu_seqlens is None else cu_seqlens.numel() - 1
-    _expect(S0, "S0", (NS, Hv, Dk, Dv), torch.float32, dev)
-    _expect(S_T, "S_T", (NS, Hv, Dk, Dv), torch.float32, dev)
-    _expect(o, "o", (B, T, Hv, Dv), io, dev)
-    _expect(A_log, "A_log", (Hv,), torch.float32, dev)
-    _expect(dt_bias, "dt_bias", (Hv,), torch.float32, dev)
-    a.B, a.T, a.Hk, a.Hv, a.Dk, a.Dv = B, T, Hk, Hv, Dk, Dv
-    a.flags = _lib._flags(l2norm_qk, beta_logits)
-    a.l2_eps, a.scale = eps, scale
-    a.q, a.q_stride = _rows(q, "q")
-    a.k, a.k_stride = _rows(k, "k")
-    a.v, a.v_stride = _rows(v, "v")
-    p = _lib._ptr
-    a.g, a.beta, a.S0, a.o, a.S_T = p(g), p(beta), p(S0), p(o), p(S_T)
-    a.A_log, a.dt_bias = p(A_log), p(dt_bias)
+    qs, vs = q.shape, v.shape
+    B, T, Hk, Dk = qs
+    Hv, Dv = vs[2:]
+    io, dev, f32 = q.dtype, q.device, torch.float32
+    gates = (B, T, Hv)
+    cu, n, NS = None, 0, B
     if cu_seqlens is not None:
-        a.cu_seqlens = _int32(cu_seqlens, "cu_seqlens", dev)
-        a.n_seqs = NS
-    return a
+        cu, NS = _list(cu_seqlens, "cu_seqlens", dev), cu_seqlens.numel() - 1
+        n = NS
+    state = (NS, Hv, Dk, Dv)
+    pq, sq = _rows(q, "q", qs, io, dev)
+    pk, sk = _rows(k, "k", qs, io, dev)
+    pv, sv = _rows(v, "v", torch.Size((B, T, Hv, Dv)), io, dev)
+    return GdrArgs(B, T, Hk, Hv, Dk, Dv, _lib._flags(l2norm_qk, beta_logits), eps, scale, _lib._io_of(q),
+                   sq, sk, sv, pq, pk, pv, _dense(g, "g", gates, io, dev), _dense(beta, "beta", gates, io, dev),
+                   _dense(S0, "S0", state, f32, dev), _dense(o, "o", vs, io, dev),
+                   _dense(S_T, "S_T", state, f32, dev), _dense(A_log, "A_log", (Hv,), f32, dev),
+                   _dense(dt_bias, "dt_bias", (Hv,), f32, dev), cu, n)
 
 
 def kda_validate_gdr_prefill(args: GdrArgs) -> int:
@@ -208,32 +217,39 @@ def kda_gdr_prefill(q, k, v, g, beta, S0=None, *, scale=1.0, l2norm_qk=True, eps
     beta holds logits.  Packed sequences: cu_seqlens int32 [N + 1] on the device
     with B = 1; then S0, S_T are [N, Hv, Dk, Dv].
     """
+    away = _elsewhere(q)
+    if away is not None:
+        with away:
+            return kda_gdr_prefill(q, k, v, g, beta, S0, scale=scale, l2norm_qk=l2norm_qk, eps=eps, A_log=A_log,
+                                   dt_bias=dt_bias, beta_logits=beta_logits, cu_seqlens=cu_seqlens, o=o, S_T=S_T,
+                                   workspace=workspace, stream=stream)
     dev = q.device
-    with _device(q):
-        st = _stream(stream, dev)
+    if o is None:
+        o = torch.empty(v.shape, dtype=q.dtype, device=dev)
+        if stream is not None:
+            _used(stream, o)
+    if S_T is None:
         NS = q.shape[0] if cu_seqlens is None else cu_seqlens.numel() - 1
-        if o is None:
-            o = torch.empty(v.shape, dtype=q.dtype, device=dev)
-            _used(st, o)
-        if S_T is None:
-            S_T = torch.empty(NS, v.shape[2], q.shape[3], v.shape[3], dtype=torch.float32, device=dev)
-            _used(st, S_T)
-        a = gdr_args(q, k, v, g, beta, S0, o, S_T, scale=scale, l2norm_qk=l2norm_qk, eps=eps,
-                     A_log=A_log, dt_bias=dt_bias, beta_logits=beta_logits, cu_seqlens=cu_seqlens)
-        lib = _lib.load()
-        ws = _scratch(lib.kda_gdr_prefill_workspace_bytes(ctypes.byref(a)), dev, st, workspace)
-        _lib._check(lib.kda_gdr_prefill(ctypes.byref(a), *_ws(ws), _handle(st)), "kda_gdr_prefill")
+        S_T = torch.empty(NS, v.shape[2], q.shape[3], v.shape[3], dtype=torch.float32, device=dev)
+        if stream is not None:
+            _used(stream, S_T)
+    a = ctypes.byref(gdr_args(q, k, v, g, beta, S0, o, S_T, scale=scale, l2norm_qk=l2norm_qk, eps=eps,
+                              A_log=A_log, dt_bias=dt_bias, beta_logits=beta_logits, cu_seqlens=cu_seqlens))
+    lib = _lib.load()
+    ws, keep = _scratch(lib.kda_gdr_prefill_workspace_bytes(a), dev, stream, workspace)
+    status = lib.kda_gdr_prefill(a, *ws, _handle(stream, dev))
+    if status:
+        _lib._check(status, "kda_gdr_prefill")
     return o, S_T
 
 
 # ------------------------------------------------------------------ backward
+_GRADS = ("dq", "dk", "dv", "dg", "dbeta", "dS0", "dA_log", "ddt_bias")
+
+
 def gdr_backward_args(fwd: GdrArgs, do, dS_T, grads: dict) -> GdrBackwardArgs:
-    a = GdrBackwardArgs()
-    a.fwd = fwd
-    a.dO, a.dS_T = _lib._ptr(do), _lib._ptr(dS_T)
-    for n in ("dq", "dk", "dv", "dg", "dbeta", "dS0", "dA_log", "ddt_bias"):
-        setattr(a, n, _lib._ptr(grads.get(n)))
-    return a
+    """Fill kda_gdr_backward_args (grads: the outputs by name)."""
+    return GdrBackwardArgs(fwd, _lib._ptr(do), _lib._ptr(dS_T), *(_lib._ptr(grads.get(n)) for n in _GRADS))
 
 
 def kda_validate_gdr_backward(args: GdrBackwardArgs) -> int:
@@ -258,33 +274,41 @@ def kda_gdr_prefill_backward(q, k, v, g, beta, S0=None, *, do, dS_T=None, scale=
     [B, T, Hv] in the inputs' type, dS0 fp32, and with A_log the fp32 dA_log and
     ddt_bias [Hv] (dg and dbeta are then those of the raw projection and logits).
     Tokens outside every packed sequence get zero gradients."""
+    away = _elsewhere(q)
+    if away is not None:
+        with away:
+            return kda_gdr_prefill_backward(q, k, v, g, beta, S0, do=do, dS_T=dS_T, scale=scale, l2norm_qk=l2norm_qk,
+                                            eps=eps, A_log=A_log, dt_bias=dt_bias, beta_logits=beta_logits,
+                                            cu_seqlens=cu_seqlens, workspace=workspace, stream=stream)
     dev, io = q.device, q.dtype
     B, T, Hk, Dk = q.shape
     Hv, Dv = v.shape[2:]
     NS = B if cu_seqlens is None else cu_seqlens.numel() - 1
-    with _device(q):
-        st = _stream(stream, dev)
-        fwd = gdr_args(q, k, v, g, beta, S0, None, None, scale=scale, l2norm_qk=l2norm_qk, eps=eps,
-                       A_log=A_log, dt_bias=dt_bias, beta_logits=beta_logits, cu_seqlens=cu_seqlens)
-        _expect(do, "do", (B, T, Hv, Dv), io, dev)
-        _expect(dS_T, "dS_T", (NS, Hv, Dk, Dv), torch.float32, dev)
-        # packed offsets may leave tokens out: those gradients are not written
-        new = torch.empty if cu_seqlens is None else torch.zeros
-        grads = dict(dq=new(B, T, Hk, Dk, dtype=io, device=dev), dk=new(B, T, Hk, Dk, dtype=io, device=dev),
-                     dv=new(B, T, Hv, Dv, dtype=io, device=dev), dg=new(B, T, Hv, dtype=io, device=dev),
-                     dbeta=new(B, T, Hv, dtype=io, device=dev),
-                     dS0=torch.empty(NS, Hv, Dk, Dv, dtype=torch.float32, device=dev))
-        if A_log is not None:
-            grads["dA_log"] = torch.empty(Hv, dtype=torch.float32, device=dev)
-            grads["ddt_bias"] = torch.empty(Hv, dtype=torch.float32, device=dev)
-        if isinstance(st, torch.cuda.Stream) and cu_seqlens is not None:
-            st.wait_stream(torch.cuda.current_stream(dev))  # the zeros
-        _used(st, *grads.values())
-        a = gdr_backward_args(fwd, do, dS_T, grads)
-        lib = _lib.load()
-        ws = _scratch(lib.kda_gdr_backward_workspace_bytes(ctypes.byref(a)), dev, st, workspace)
-        _lib._check(lib.kda_gdr_prefill_backward(ctypes.byref(a), *_ws(ws), _handle(st)),
-                    "kda_gdr_prefill_backward")
+    fwd = gdr_args(q, k, v, g, beta, S0, None, None, scale=scale, l2norm_qk=l2norm_qk, eps=eps, A_log=A_log,
+                   dt_bias=dt_bias, beta_logits=beta_logits, cu_seqlens=cu_seqlens)
+    if cu_seqlens is None:
+        new = torch.empty
+    else:  # packed offsets may leave tokens out: those gradients are not written
+        new = torch.zeros
+    grads = dict(dq=new(B, T, Hk, Dk, dtype=io, device=dev), dk=new(B, T, Hk, Dk, dtype=io, device=dev),
+                 dv=new(B, T, Hv, Dv, dtype=io, device=dev), dg=new(B, T, Hv, dtype=io, device=dev),
+                 dbeta=new(B, T, Hv, dtype=io, device=dev),
+                 dS0=torch.empty(NS, Hv, Dk, Dv, dtype=torch.float32, device=dev))
+    if A_log is not None:
+        grads["dA_log"] = torch.empty(Hv, dtype=torch.float32, device=dev)
+        grads["ddt_bias"] = torch.empty(Hv, dtype=torch.float32, device=dev)
+    if stream is not None:
+        if cu_seqlens is not None:
+            _after_fill(stream, dev)
+        _used(stream, *grads.values())
+    a = GdrBackwardArgs(fwd, _dense(do, "do", v.shape, io, dev),
+                        _dense(dS_T, "dS_T", (NS, Hv, Dk, Dv), torch.float32, dev),
+                        *(_lib._ptr(grads.get(n)) for n in _GRADS))
+    lib = _lib.load()
+    r = ctypes.byref(a)
+    _lib._check(lib.kda_validate_gdr_backward(r), "kda_gdr_prefill_backward")
+    ws, keep = _scratch(lib.kda_gdr_backward_workspace_bytes(r), dev, stream, workspace)
+    _lib._check(lib.kda_gdr_prefill_backward(r, *ws, _handle(stream, dev)), "kda_gdr_prefill_backward")
     return grads
 
 
@@ -292,33 +316,24 @@ def kda_gdr_prefill_backward(q, k, v, g, beta, S0=None, *, do, dS_T=None, scale=
 def gdr_decode_args(q, k, v, g, beta, S, slots=None, o=None, *, scale=1.0, l2norm_qk=True, eps=1e-6,
                     A_log=None, dt_bias=None, beta_logits=False) -> GdrDecodeArgs:
     """Fill kda_gdr_decode_args from tensors (shapes as kda_gdr_decode)."""
-    N, Hk, Dk = q.shape
-    Hv, Dv = v.shape[1:]
-    io, dev = q.dtype, q.device
-    a = GdrDecodeArgs()
-    a.io = _lib._io_of(q)
-    _expect(k, "k", (N, Hk, Dk), io, dev)
-    _expect(v, "v", (N, Hv, Dv), io, dev)
-    _expect(g, "g", (N, Hv), io, dev)
-    _expect(beta, "beta", (N, Hv), io, dev)
-    _expect(S, "S", (S.shape[0], Hv, Dk, Dv), torch.float32, dev)
-    _expect(o, "o", (N, Hv, Dv), io, dev)
-    _expect(A_log, "A_log", (Hv,), torch.float32, dev)
-    _expect(dt_bias, "dt_bias", (Hv,), torch.float32, dev)
-    a.N, a.n_slots, a.Hk, a.Hv, a.Dk, a.Dv = N, S.shape[0], Hk, Hv, Dk, Dv
-    a.flags = _lib._flags(l2norm_qk, beta_logits)
-    a.l2_eps, a.scale = eps, scale
-    a.q, a.q_stride = _rows(q, "q")
-    a.k, a.k_stride = _rows(k, "k")
-    a.v, a.v_stride = _rows(v, "v")
-    p = _lib._ptr
-    a.g, a.beta, a.S, a.o = p(g), p(beta), p(S), p(o)
-    a.A_log, a.dt_bias = p(A_log), p(dt_bias)
+    qs, vs = q.shape, v.shape
+    N, Hk, Dk = qs
+    Hv, Dv = vs[1:]
+    io, dev, f32 = q.dtype, q.device, torch.float32
+    at = None
     if slots is not None:
-        if tuple(slots.shape) != (N,):
+        if slots.shape != (N,):
             raise ValueError(f"slots has shape {tuple(slots.shape)}, expected {(N,)}")
-        a.slots = _int32(slots, "slots", dev)
-    return a
+        at = _list(slots, "slots", dev)
+    pq, sq = _rows(q, "q", qs, io, dev)
+    pk, sk = _rows(k, "k", qs, io, dev)
+    pv, sv = _rows(v, "v", torch.Size((N, Hv, Dv)), io, dev)
+    n = S.shape[0]
+    return GdrDecodeArgs(N, n, Hk, Hv, Dk, Dv, _lib._flags(l2norm_qk, beta_logits), eps, scale, _lib._io_of(q),
+                         sq, sk, sv, pq, pk, pv, _dense(g, "g", (N, Hv), io, dev),
+                         _dense(beta, "beta", (N, Hv), io, dev), _dense(A_log, "A_log", (Hv,), f32, dev),
+                         _dense(dt_bias, "dt_bias", (Hv,), f32, dev), _dense(S, "S", (n, Hv, Dk, Dv), f32, dev),
+                         at, _dense(o, "o", vs, io, dev))
 
 
 def kda_validate_gdr_decode(args: GdrDecodeArgs) -> int:
@@ -337,18 +352,22 @@ def kda_gdr_decode(q, k, v, g, beta, S, slots=None, *, scale=1.0, l2norm_qk=True
     o is left as it was -- zeros if o is allocated here).  Rows with one slot are
     consecutive tokens of its sequence.  q, k [N, Hk, Dk], v [N, Hv, Dv], g, beta
     [N, Hv].  Returns o [N, Hv, Dv]."""
+    away = _elsewhere(q)
+    if away is not None:
+        with away:
+            return kda_gdr_decode(q, k, v, g, beta, S, slots, scale=scale, l2norm_qk=l2norm_qk, eps=eps, A_log=A_log,
+                                  dt_bias=dt_bias, beta_logits=beta_logits, o=o, stream=stream)
     dev = q.device
-    with _device(q):
-        st = _stream(stream, dev)
-        if o is None:
-            new = torch.empty if slots is None else torch.zeros
-            o = new(v.shape, dtype=q.dtype, device=dev)
-            _used(st, o)
-            if isinstance(st, torch.cuda.Stream) and slots is not None:
-                st.wait_stream(torch.cuda.current_stream(dev))  # the zeros
-        a = gdr_decode_args(q, k, v, g, beta, S, slots, o, scale=scale, l2norm_qk=l2norm_qk, eps=eps,
-                            A_log=A_log, dt_bias=dt_bias, beta_logits=beta_logits)
-        _lib._check(_lib.load().kda_gdr_decode(ctypes.byref(a), _handle(st)), "kda_gdr_decode")
+    if o is None:
+        o = (torch.empty if slots is None else torch.zeros)(v.shape, dtype=q.dtype, device=dev)
+        if stream is not None:
+            _used(stream, o)
+            _after_fill(stream, dev)
+    a = gdr_decode_args(q, k, v, g, beta, S, slots, o, scale=scale, l2norm_qk=l2norm_qk, eps=eps, A_log=A_log,
+                        dt_bias=dt_bias, beta_logits=beta_logits)
+    status = _lib.load().kda_gdr_decode(ctypes.byref(a), _handle(stream, dev))
+    if status:
+        _lib._check(status, "kda_gdr_decode")
     return o
 
 
@@ -358,16 +377,13 @@ def pages_pool(pool) -> PagesPool:
     layers may be further apart)."""
     if pool.dim() < 3:
         raise ValueError("a pool is [layers, pages, ...]")
-    page = pool[0, 0]
-    if not page.is_contiguous() or (pool.shape[1] > 1 and pool.stride(1) != page.numel()):
-        raise ValueError("the pages of a layer must be dense")
-    es = pool.element_size()
-    p = PagesPool()
-    p.data = pool.data_ptr()
-    p.page_bytes = page.numel() * es
-    p.layer_stride = pool.stride(0) * es if pool.shape[0] > 1 else 0
-    p.n_layers, p.n_pages = pool.shape[:2]
-    return p
+    shape, es, layer = pool.shape, pool.element_size(), 0
+    page = shape[2:].numel()
+    if not pool.is_contiguous():
+        if not pool[0, 0].is_contiguous() or (shape[1] > 1 and pool.stride(1) != page):
+            raise ValueError("the pages of a layer must be dense")
+        layer = pool.stride(0) * es if shape[0] > 1 else 0
+    return PagesPool(pool.data_ptr(), layer, page * es, shape[0], shape[1])
 
 
 def kda_pages_workspace_bytes(pool: PagesPool, n: int) -> int:
@@ -378,41 +394,46 @@ def kda_pages_fork(pool, refs, src, *, refs_out=None, dst=None, workspace=None, 
     """Forks pages of `pool` [layers, pages, ...]: request i gets the next free page
     (refs[p] <= 0), filled from page src[i] (zeros where -1).  Returns (dst, refs_out):
     the pages (-1 where a request could not be met) and the new counts."""
-    dev = pool.device
-    with _device(pool):
-        st = _stream(stream, dev)
-        p = pages_pool(pool)
-        _expect(refs, "refs", (p.n_pages,), torch.int32, dev)
-        _expect(refs_out, "refs_out", (p.n_pages,), torch.int32, dev)
-        n = src.numel()
-        _expect(dst, "dst", (n,), torch.int32, dev)
-        if refs_out is None:
-            refs_out = torch.empty_like(refs)
-            _used(st, refs_out)
-        if dst is None:
-            dst = torch.empty(n, dtype=torch.int32, device=dev)
-            _used(st, dst)
-        ws = _scratch(kda_pages_workspace_bytes(p, n), dev, st, workspace)
-        _lib._check(_lib.load().kda_pages_fork(ctypes.byref(p), _lib._ptr(refs), _lib._ptr(refs_out),
-                                               _int32(src, "src", dev), _lib._ptr(dst), n, *_ws(ws),
-                                               _handle(st)), "kda_pages_fork")
+    away = _elsewhere(pool)
+    if away is not None:
+        with away:
+            return kda_pages_fork(pool, refs, src, refs_out=refs_out, dst=dst, workspace=workspace, stream=stream)
+    dev, i32 = pool.device, torch.int32
+    p = pages_pool(pool)
+    n, pages = src.numel(), (p.n_pages,)
+    if refs_out is None:
+        refs_out = torch.empty(pages, dtype=i32, device=dev)
+        if stream is not None:
+            _used(stream, refs_out)
+    if dst is None:
+        dst = torch.empty(n, dtype=i32, device=dev)
+        if stream is not None:
+            _used(stream, dst)
+    r, lib = ctypes.byref(p), _lib.load()
+    ws, keep = _scratch(lib.kda_pages_workspace_bytes(r, n), dev, stream, workspace)
+    _lib._check(lib.kda_pages_fork(r, _dense(refs, "refs", pages, i32, dev),
+                                   _dense(refs_out, "refs_out", pages, i32, dev), _list(src, "src", dev),
+                                   _dense(dst, "dst", (n,), i32, dev), n, *ws, _handle(stream, dev)),
+                "kda_pages_fork")
     return dst, refs_out
 
 
 def kda_pages_free(refs, pages, *, refs_out=None, stream=None):
     """Lowers the count of every listed page (once for each time it is listed, not
     below 0).  Returns refs_out."""
-    dev = refs.device
-    with _device(refs):
-        st = _stream(stream, dev)
-        _expect(refs, "refs", (refs.numel(),), torch.int32, dev)
-        _expect(refs_out, "refs_out", (refs.numel(),), torch.int32, dev)
-        if refs_out is None:
-            refs_out = torch.empty_like(refs)
-            _used(st, refs_out)
-        _lib._check(_lib.load().kda_pages_free(_lib._ptr(refs), _lib._ptr(refs_out), refs.numel(),
-                                               _int32(pages, "pages", dev), pages.numel(), _handle(st)),
-                    "kda_pages_free")
+    away = _elsewhere(refs)
+    if away is not None:
+        with away:
+            return kda_pages_free(refs, pages, refs_out=refs_out, stream=stream)
+    dev, i32, shape = refs.device, torch.int32, (refs.numel(),)
+    if refs_out is None:
+        refs_out = torch.empty(shape, dtype=i32, device=dev)
+        if stream is not None:
+            _used(stream, refs_out)
+    _lib._check(_lib.load().kda_pages_free(_dense(refs, "refs", shape, i32, dev),
+                                           _dense(refs_out, "refs_out", shape, i32, dev), shape[0],
+                                           _list(pages, "pages", dev), pages.numel(), _handle(stream, dev)),
+                "kda_pages_free")
     return refs_out
 
 
@@ -421,30 +442,35 @@ def kda_pages_compact(pool, refs, table=None, *, refs_out=None, new_id=None, tab
     """Moves the pages in use to the front of the pool.  Returns (n_used [1],
     new_id, refs_out, table_out): the new index of every page (-1: free), the new
     counts, and the table's entries renamed (None without a table)."""
-    dev = pool.device
-    with _device(pool):
-        st = _stream(stream, dev)
-        p = pages_pool(pool)
-        _expect(refs, "refs", (p.n_pages,), torch.int32, dev)
-        _expect(refs_out, "refs_out", (p.n_pages,), torch.int32, dev)
-        _expect(new_id, "new_id", (p.n_pages,), torch.int32, dev)
-        if refs_out is None:
-            refs_out = torch.empty_like(refs)
-        if new_id is None:
-            new_id = torch.empty_like(refs)
-        n_used = torch.empty(1, dtype=torch.int32, device=dev)
-        n = 0
-        if table is not None:
-            _int32(table, "table", dev)
-            n = table.numel()
-            if table_out is None:
-                table_out = torch.empty_like(table)
-            _expect(table_out, "table_out", table.shape, torch.int32, dev)
-        _used(st, refs_out, new_id, n_used, table_out)
-        ws = _scratch(kda_pages_workspace_bytes(p, 0), dev, st, workspace)
-        _lib._check(_lib.load().kda_pages_compact(
-            ctypes.byref(p), _lib._ptr(refs), _lib._ptr(refs_out), _lib._ptr(new_id), _lib._ptr(n_used),
-            _lib._ptr(table), _lib._ptr(table_out), n, *_ws(ws), _handle(st)), "kda_pages_compact")
+    away = _elsewhere(pool)
+    if away is not None:
+        with away:
+            return kda_pages_compact(pool, refs, table, refs_out=refs_out, new_id=new_id, table_out=table_out,
+                                     workspace=workspace, stream=stream)
+    dev, i32 = pool.device, torch.int32
+    p = pages_pool(pool)
+    pages = (p.n_pages,)
+    if refs_out is None:
+        refs_out = torch.empty(pages, dtype=i32, device=dev)
+    if new_id is None:
+        new_id = torch.empty(pages, dtype=i32, device=dev)
+    n_used = torch.empty(1, dtype=i32, device=dev)
+    n, tab = 0, None
+    if table is not None:
+        n, tab = table.numel(), _list(table, "table", dev)
+        if table_out is None:
+            table_out = torch.empty(table.shape, dtype=i32, device=dev)
+    else:
+        table_out = None
+    if stream is not None:
+        _used(stream, refs_out, new_id, n_used, table_out)
+    r, lib = ctypes.byref(p), _lib.load()
+    ws, keep = _scratch(lib.kda_pages_workspace_bytes(r, 0), dev, stream, workspace)
+    _lib._check(lib.kda_pages_compact(
+        r, _dense(refs, "refs", pages, i32, dev), _dense(refs_out, "refs_out", pages, i32, dev),
+        _dense(new_id, "new_id", pages, i32, dev), n_used.data_ptr(), tab,
+        _dense(table_out, "table_out", table.shape if table is not None else (), i32, dev), n, *ws,
+        _handle(stream, dev)), "kda_pages_compact")
     return n_used, new_id, refs_out, table_out
 
 
@@ -452,21 +478,24 @@ def kda_pages_copy(src_pool, dst_pool, src, dst, *, done=None, workspace=None, s
     """Copies page src[i] of src_pool to page dst[i] of dst_pool (zeros where src[i]
     is -1) in every layer.  Returns done [n]: 1 where the pair was copied, 0 where it
     was left out (include/kda.h says which)."""
+    away = _elsewhere(dst_pool)
+    if away is not None:
+        with away:
+            return kda_pages_copy(src_pool, dst_pool, src, dst, done=done, workspace=workspace, stream=stream)
     dev = dst_pool.device
     if src_pool.device != dev:
         raise ValueError("both pools must be on one device")
-    with _device(dst_pool):
-        st = _stream(stream, dev)
-        ps, pd = pages_pool(src_pool), pages_pool(dst_pool)
-        n = src.numel()
-        if dst.numel() != n:
-            raise ValueError("src and dst differ in length")
-        if done is None:
-            done = torch.empty(n, dtype=torch.int32, device=dev)
-            _used(st, done)
-        _expect(done, "done", (n,), torch.int32, dev)
-        ws = _scratch(kda_pages_workspace_bytes(pd, n), dev, st, workspace)
-        _lib._check(_lib.load().kda_pages_copy(ctypes.byref(ps), ctypes.byref(pd), _int32(src, "src", dev),
-                                               _int32(dst, "dst", dev), _lib._ptr(done), n, *_ws(ws),
-                                               _handle(st)), "kda_pages_copy")
+    ps, pd = pages_pool(src_pool), pages_pool(dst_pool)
+    n = src.numel()
+    if dst.numel() != n:
+        raise ValueError("src and dst differ in length")
+    if done is None:
+        done = torch.empty(n, dtype=torch.int32, device=dev)
+        if stream is not None:
+            _used(stream, done)
+    lib = _lib.load()
+    ws, keep = _scratch(lib.kda_pages_workspace_bytes(ctypes.byref(pd), n), dev, stream, workspace)
+    _lib._check(lib.kda_pages_copy(ctypes.byref(ps), ctypes.byref(pd), _list(src, "src", dev), _list(dst, "dst", dev),
+                                   _dense(done, "done", (n,), torch.int32, dev), n, *ws, _handle(stream, dev)),
+                "kda_pages_copy")
     return done
