@@ -68,8 +68,9 @@ struct GdrShape {
   SeqTables seqs;    // bounds NULL: equal lengths
 };
 
-// Waves (of 16 value columns each) in a walk's workgroup.
-constexpr int gdr_walk_waves(int Dv, bool fp32) { return Dv >= 128 ? (fp32 ? 4 : 8) : Dv / 16; }
+// Whether a walk's workgroup takes 128 value columns (8 waves) or 64 (4 waves) with
+// bf16 inputs; LDS holds one workgroup of either.
+constexpr bool gdr_whole_head(long walks, int Dv) { return Dv % 128 == 0 && walks > 128; }
 
 struct GdrPrepParams {
   GdrShape s;

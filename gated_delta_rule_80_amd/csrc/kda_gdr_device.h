@@ -117,41 +117,58 @@ __device__ __forceinline__ f32x4 g_colp(const float* img, int u, int tile, int r
   for (int e = 0; e < 4; ++e) f[e] = img[GImg<float, K>::at(16 * u + 4 * g + e, 16 * tile + r)];
   return f;
 }
-// Both units of the two tiles 2 jj, 2 jj + 1 of the columns of a 64-row bf16 image,
-// as the transposing reads with their wait in one block: the compiler has a
-// transposing read that it can see wait for every global-to-LDS copy in flight, the
-// next chunk's included.  The rows' swizzle depends on the lane only, so one
-// address serves all eight reads.
-template <int K>
-__device__ __forceinline__ void g_colp_pair(const __bf16* img, int jj, int r, int g, bf16x8 (&t0)[2], bf16x8 (&t1)[2]) {
-  typedef __attribute__((address_space(3))) const __bf16 lds_bf16;
-  const uint32_t at = (uint32_t)(uintptr_t)(lds_bf16*)(img + GImg<__bf16, K>::at(8 * g + (r >> 2), 32 * jj + 8 * (r & 3)));
-  bf16x4 a, b, c, d, e, f, x, y;
-  asm volatile(
-      "ds_read_b64_tr_b16 %0, %8\n\t"
-      "ds_read_b64_tr_b16 %1, %8 offset:%9\n\t"
-      "ds_read_b64_tr_b16 %2, %8 offset:%10\n\t"
-      "ds_read_b64_tr_b16 %3, %8 offset:%11\n\t"
-      "ds_read_b64_tr_b16 %4, %8 offset:8\n\t"
-      "ds_read_b64_tr_b16 %5, %8 offset:%12\n\t"
-      "ds_read_b64_tr_b16 %6, %8 offset:%13\n\t"
-      "ds_read_b64_tr_b16 %7, %8 offset:%14\n\t"
-      "s_waitcnt lgkmcnt(0)"
-      : "=&v"(a), "=&v"(b), "=&v"(c), "=&v"(d), "=&v"(e), "=&v"(f), "=&v"(x), "=&v"(y)
-      : "v"(at), "n"(4 * K * 2), "n"(32 * K * 2), "n"(36 * K * 2), "n"(4 * K * 2 + 8), "n"(32 * K * 2 + 8),
-        "n"(36 * K * 2 + 8));
-  t0[0] = __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7);
-  t0[1] = __builtin_shufflevector(c, d, 0, 1, 2, 3, 4, 5, 6, 7);
-  t1[0] = __builtin_shufflevector(e, f, 0, 1, 2, 3, 4, 5, 6, 7);
-  t1[1] = __builtin_shufflevector(x, y, 0, 1, 2, 3, 4, 5, 6, 7);
+// Unit u of N tiles from tile t0 on (t0 even, N = 2 or 4) of the columns of a bf16
+// image: the transposing reads with their wait in one block, because the compiler has
+// a transposing read that it can see wait for every global-to-LDS copy in flight, the
+// next chunk's included.
+__device__ __forceinline__ bf16x8 join4(bf16x4 a, bf16x4 b) {
+  return __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7);
 }
 template <int K>
-__device__ __forceinline__ void g_colp_pair(const float* img, int jj, int r, int g, f32x4 (&t0)[2], f32x4 (&t1)[2]) {
+__device__ __forceinline__ void g_colp_tiles(const __bf16* img, int u, int t0, int r, int g, bf16x8 (&f)[2]) {
+  typedef __attribute__((address_space(3))) const __bf16 lds_bf16;
+  const int row = 32 * u + 8 * g + (r >> 2), c = 16 * t0 + 8 * (r & 3);
+  const uint32_t a0 = (uint32_t)(uintptr_t)(lds_bf16*)(img + GImg<__bf16, K>::at(row, c));
+  bf16x4 x0, x1, x2, x3;
+  asm volatile(
+      "ds_read_b64_tr_b16 %0, %4\n\t"
+      "ds_read_b64_tr_b16 %1, %4 offset:%5\n\t"
+      "ds_read_b64_tr_b16 %2, %4 offset:8\n\t"
+      "ds_read_b64_tr_b16 %3, %4 offset:%6\n\t"
+      "s_waitcnt lgkmcnt(0)"
+      : "=&v"(x0), "=&v"(x1), "=&v"(x2), "=&v"(x3)
+      : "v"(a0), "n"(4 * K * 2), "n"(4 * K * 2 + 8));
+  f[0] = join4(x0, x1);
+  f[1] = join4(x2, x3);
+}
+template <int K>
+__device__ __forceinline__ void g_colp_tiles(const __bf16* img, int u, int t0, int r, int g, bf16x8 (&f)[4]) {
+  typedef __attribute__((address_space(3))) const __bf16 lds_bf16;
+  const int row = 32 * u + 8 * g + (r >> 2), c = 16 * t0 + 8 * (r & 3);
+  const uint32_t a0 = (uint32_t)(uintptr_t)(lds_bf16*)(img + GImg<__bf16, K>::at(row, c));
+  const uint32_t a1 = (uint32_t)(uintptr_t)(lds_bf16*)(img + GImg<__bf16, K>::at(row, c + 32));
+  bf16x4 x0, x1, x2, x3, y0, y1, y2, y3;
+  asm volatile(
+      "ds_read_b64_tr_b16 %0, %8\n\t"
+      "ds_read_b64_tr_b16 %1, %8 offset:%10\n\t"
+      "ds_read_b64_tr_b16 %2, %8 offset:8\n\t"
+      "ds_read_b64_tr_b16 %3, %8 offset:%11\n\t"
+      "ds_read_b64_tr_b16 %4, %9\n\t"
+      "ds_read_b64_tr_b16 %5, %9 offset:%10\n\t"
+      "ds_read_b64_tr_b16 %6, %9 offset:8\n\t"
+      "ds_read_b64_tr_b16 %7, %9 offset:%11\n\t"
+      "s_waitcnt lgkmcnt(0)"
+      : "=&v"(x0), "=&v"(x1), "=&v"(x2), "=&v"(x3), "=&v"(y0), "=&v"(y1), "=&v"(y2), "=&v"(y3)
+      : "v"(a0), "v"(a1), "n"(4 * K * 2), "n"(4 * K * 2 + 8));
+  f[0] = join4(x0, x1);
+  f[1] = join4(x2, x3);
+  f[2] = join4(y0, y1);
+  f[3] = join4(y2, y3);
+}
+template <int K, int N>
+__device__ __forceinline__ void g_colp_tiles(const float* img, int u, int t0, int r, int g, f32x4 (&f)[N]) {
 #pragma unroll
-  for (int u = 0; u < 2; ++u) {
-    t0[u] = g_colp<K>(img, u, 2 * jj, r, g);
-    t1[u] = g_colp<K>(img, u, 2 * jj + 1, r, g);
-  }
+  for (int t = 0; t < N; ++t) f[t] = g_colp<K>(img, u, t0 + t, r, g);
 }
 // columns m0 + lane
 template <int K>
@@ -184,10 +201,42 @@ __device__ __forceinline__ f32x4 g_acc(const float* img, int tile, int m0, int r
   return f;
 }
 
+// The same kept as read until it is used.
+template <typename E> struct AccRaw;
+template <> struct AccRaw<__bf16> {
+  bf16x4 v;
+  template <int K> __device__ __forceinline__ void load(const __bf16* img, int tile, int m0, int r, int g) {
+    typedef __attribute__((address_space(3))) bf16x4 lds_bf16x4;
+    v = __builtin_amdgcn_ds_read_tr16_b64_v4bf16(
+        (lds_bf16x4*)(img + GImg<__bf16, K>::at(GOp<__bf16>::row4(tile, g) + (r >> 2), m0 + 4 * (r & 3))));
+  }
+  __device__ __forceinline__ float operator[](int e) const { return (float)v[e]; }
+};
+template <> struct AccRaw<float> {
+  f32x4 v;
+  template <int K> __device__ __forceinline__ void load(const float* img, int tile, int m0, int r, int g) {
+    v = g_acc<K>(img, tile, m0, r, g);
+  }
+  __device__ __forceinline__ float operator[](int e) const { return v[e]; }
+};
+
 // NT terms of one unit of a float32 quantity held in accumulators.
 template <typename E, int NT> struct Terms;
 typedef float f32x2 __attribute__((ext_vector_type(2)));
 typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+// x - h[0] and x - h[1] as one instruction each (a two-element dot product with -1
+// and 0; exact, as the rest of a rounding is representable).  The factors are kept in
+// a register: as an inline constant -1.0 the instruction takes the other half.
+__device__ __forceinline__ uint32_t pair_factor(uint32_t bits) {
+  asm("" : "+s"(bits));
+  return bits;
+}
+__device__ __forceinline__ float minus_low(bf16x2 h, float x) {
+  return __builtin_amdgcn_fdot2_f32_bf16(h, __builtin_bit_cast(bf16x2, pair_factor(0x0000bf80u)), x, false);
+}
+__device__ __forceinline__ float minus_high(bf16x2 h, float x) {
+  return __builtin_amdgcn_fdot2_f32_bf16(h, __builtin_bit_cast(bf16x2, pair_factor(0xbf800000u)), x, false);
+}
 template <int NT> struct Terms<__bf16, NT> {
   static constexpr int N = NT;
   bf16x8 t[NT];
@@ -201,8 +250,8 @@ template <int NT> struct Terms<__bf16, NT> {
         t[n][2 * q] = h[0];
         t[n][2 * q + 1] = h[1];
         if (n + 1 < NT) {
-          x[0] -= (float)h[0];
-          x[1] -= (float)h[1];
+          x[0] = minus_low(h, x[0]);
+          x[1] = minus_high(h, x[1]);
         }
       }
     }
