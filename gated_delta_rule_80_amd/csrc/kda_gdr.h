@@ -68,6 +68,24 @@ struct GdrShape {
   SeqTables seqs;    // bounds NULL: equal lengths
 };
 
+// The split of B equal-length rows of nch chunks: segments per walk and their length.
+// It triples the work of a chunk (two maps, then the outputs) for nseg times the
+// parallelism, so it pays from 6 segments on, while workgroups stay within the 256
+// CUs; segments of at least 4 chunks keep the composition (about 1 us a segment)
+// below the walks.  Measured at 64k tokens, 12 heads, D = 128, bf16: 2.88 ms unsplit.
+struct GdrSplit {
+  int nseg, seg_len;
+};
+constexpr GdrSplit gdr_split(long walks, int nch, int Dv, bool fp32) {
+  const long vb = Dv >= 128 && !fp32 ? 128 : (Dv >= 64 ? 64 : 32);
+  long P = 256 / (walks * (Dv / vb) > 0 ? walks * (Dv / vb) : 1);
+  if (nch / 4 < P) P = nch / 4;
+  if (P > 64) P = 64;
+  if (P < 6) return {1, nch};
+  const int len = (int)((nch + P - 1) / P);
+  return {(nch + len - 1) / len, len};
+}
+
 // Whether a walk's workgroup takes 128 value columns (8 waves) or 64 (4 waves) with
 // bf16 inputs; LDS holds one workgroup of either.
 constexpr bool gdr_whole_head(long walks, int Dv) { return Dv % 128 == 0 && walks > 128; }
@@ -98,6 +116,18 @@ struct GdrWalkParams {
   // [record][Dv / 16][Dk][16], both in the element type; NULL otherwise
   void* y;
   void* ckpt;
+  // split walk (nseg > 1; equal lengths): segments of seg_len chunks walk in
+  // parallel.  The state after a run of chunks is affine in the state before it,
+  // S_end = M S_start + N, so first every segment but the last is walked from zero
+  // (the first from S0) for its N and with V = 0 from I for its M, then the starts
+  // are composed in order, then every segment is walked with its output.
+  //   starts [B Hv][nseg][Dk][Dv] float32: at index s + 1 first the N of segment s,
+  //          then the state at the start of segment s + 1 (index 0: not used)
+  //   maps   [B Hv][nseg][Dk][Dk] float32: M of segments 1 .. nseg - 2
+  int nseg, seg_len;
+  float* starts;
+  float* maps;
+  int pass;  // 0: outputs; 1: N; 2: M
 };
 
 struct GdrReverseParams {

@@ -129,8 +129,12 @@ kda_status disjoint(const Spans& outs, const Spans& ins) {
 // The workspace: sequence tables, the chunk records, and for the backward Y, the
 // two checkpoints per chunk and the float32 gradient of the decay.
 struct GdrWork {
-  size_t seq, rec, y, ckS, ckdS, dg, bytes;
+  size_t seq, rec, y, ckS, ckdS, dg, starts, maps, bytes;
 };
+GdrSplit split_of(const kda_gdr_args* a, const GdrSizes& s) {
+  if (gdr_packed(a) || a->T == 0) return {1, s.NT};
+  return gdr_split((long)a->B * a->Hv, s.NT, a->Dv, a->io == KDA_FP32);
+}
 bool gdr_work(const kda_gdr_args* a, const GdrSizes& s, bool bwd, GdrWork& w) {
   const size_t es = esize(a->io);
   size_t nrec, recs, ck = 0, y = 0, dg = 0;
@@ -148,7 +152,14 @@ bool gdr_work(const kda_gdr_args* a, const GdrSizes& s, bool bwd, GdrWork& w) {
   w.ckS = round_up(w.y + y, 256);
   w.ckdS = round_up(w.ckS + ck, 256);
   w.dg = round_up(w.ckdS + ck, 256);
-  w.bytes = round_up(w.dg + dg, 256);
+  w.starts = w.maps = round_up(w.dg + dg, 256);
+  w.bytes = w.starts;
+  if (const GdrSplit sp = split_of(a, s); !bwd && sp.nseg > 1) {
+    // at most 256 workgroups of segments: these sizes stay small
+    const size_t n = (size_t)a->B * a->Hv * sp.nseg * a->Dk * 4;
+    w.maps = w.starts + n * a->Dv;
+    w.bytes = w.maps + n * a->Dk;
+  }
   return w.bytes < (size_t(1) << 62);
 }
 
@@ -252,6 +263,11 @@ kda_status kda_gdr_prefill(const kda_gdr_args* a, void* ws, size_t ws_bytes, voi
   p.q = a->q; p.k = a->k; p.v = a->v;
   p.rec = base + w.rec;
   p.S0 = a->S0; p.S_T = a->S_T; p.o = a->o;
+  const GdrSplit sp = split_of(a, s);
+  p.nseg = sp.nseg;
+  p.seg_len = sp.seg_len;
+  p.starts = reinterpret_cast<float*>(base + w.starts);
+  p.maps = reinterpret_cast<float*>(base + w.maps);
   return hip_status(launch_gdr_walk(p, a->Dk, a->Dv, a->io == KDA_FP32, st));
 }
 

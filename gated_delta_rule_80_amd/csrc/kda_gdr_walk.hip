@@ -50,15 +50,29 @@ __global__ __launch_bounds__(64 * WV) void kda_gdr_walk_kernel(GdrWalkParams p, 
   static_assert(NUC == 2, "the slots below take the chunk in two halves");
   constexpr GdrRecord R = gdr_record(F32, CK);
   // stores of a chunk: o, 4 columns each; or the state and Y
-  constexpr int NSTORE = NV * (OUT ? TL : (F32 ? 4 : 1) * (CT + TL));
-  static_assert(OUT != CK, "the stores are counted for one or the other");
+  constexpr int NSTORE = NV * (OUT ? TL : (CK ? (F32 ? 4 : 1) * (CT + TL) : 0));
+  static_assert(!(OUT && CK), "the stores are counted for one or the other");
   __shared__ __attribute__((aligned(16))) char lds[2 * L::BYTES];
 
   const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6), r = lane & 15, g4 = lane >> 4;
-  int bh, vblk;
+  int bh, vblk, seg = 0;
   gdr_walk_id(Dv / VB, bh, vblk);
+  if (p.nseg > 1) {
+    const int walks = p.s.B * p.s.Hv;
+    seg = bh / walks + (p.pass == 2 ? 1 : 0);  // the first segment needs no M
+    bh %= walks;
+  }
   const int h = bh % p.s.Hv, b = bh / p.s.Hv, hk = h / (p.s.Hv / p.s.Hk);
-  const GdrSpan sp = gdr_span(p.s, b, h, C);
+  GdrSpan sp = gdr_span(p.s, b, h, C);
+  if (p.nseg > 1) {
+    const int c0 = seg * p.seg_len;
+    sp.tok0 += (long)c0 * C;
+    sp.Tq -= c0 * C;
+    sp.nch = sp.nch - c0 < p.seg_len ? sp.nch - c0 : p.seg_len;
+    sp.rec0 += c0 * sp.rstride;
+  }
+  // a map's M: columns of the state in place of values, and no values
+  const bool linear = !OUT && !CK && p.pass == 2;
   const int v0 = vblk * VB + 16 * NV * wave;  // this wave's value columns
   const long HD = (long)p.s.Hv * Dv;
 
@@ -82,10 +96,10 @@ __global__ __launch_bounds__(64 * WV) void kda_gdr_walk_kernel(GdrWalkParams p, 
       const IO* pv = vb + t0 * p.s.vs;
       if (last >= C - 1) {
         ck.whole(buf + L::K, pk, wave);
-        cv.whole(buf + L::V, pv, wave);
+        if (!linear) cv.whole(buf + L::V, pv, wave);
       } else {
         ck.part(buf + L::K, pk, p.s.ks, last, wave);
-        cv.part(buf + L::V, pv, p.s.vs, last, wave);
+        if (!linear) cv.part(buf + L::V, pv, p.s.vs, last, wave);
       }
     } else if (part == 1) {
       // Tm and the scalars follow one another in the record and in LDS
@@ -104,17 +118,29 @@ __global__ __launch_bounds__(64 * WV) void kda_gdr_walk_kernel(GdrWalkParams p, 
   f32x4 S[NV][CT];
   Terms<IO, 2> s2[NV][NUK];
   const size_t sbase = (size_t)bh * DK * Dv + v0 + r;
+  // where this walk's state comes from (NULL: zeros) and goes to (NULL: nowhere)
+  const size_t seg_at = ((size_t)bh * p.nseg + seg) * DK * Dv + v0 + r;
+  const float* s_in = p.S0 != nullptr && seg == 0 ? p.S0 + sbase : nullptr;
+  float* s_out = p.S_T != nullptr ? p.S_T + sbase : nullptr;
+  if (p.nseg > 1) {
+    if (p.pass == 0 && seg > 0) s_in = p.starts + seg_at;
+    if (p.pass == 0 && seg < p.nseg - 1) s_out = nullptr;
+    if (p.pass == 1) s_out = p.starts + seg_at + (size_t)DK * Dv;
+    if (p.pass == 2) s_out = p.maps + seg_at;
+  }
 #pragma unroll
   for (int v = 0; v < NV; ++v)
 #pragma unroll
-    for (int t = 0; t < CT; ++t) S[v][t] = f32x4{0.f, 0.f, 0.f, 0.f};
-  if (p.S0 != nullptr) {
+    for (int t = 0; t < CT; ++t)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) S[v][t][e] = linear && Op::row4(t, g4) + e == v0 + 16 * v + r ? 1.f : 0.f;
+  if (s_in != nullptr) {
 #pragma unroll
     for (int v = 0; v < NV; ++v)
 #pragma unroll
       for (int t = 0; t < CT; ++t)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) S[v][t][e] = p.S0[sbase + 16 * v + (size_t)(Op::row4(t, g4) + e) * Dv];
+        for (int e = 0; e < 4; ++e) S[v][t][e] = s_in[16 * v + (size_t)(Op::row4(t, g4) + e) * Dv];
   }
 #pragma unroll
   for (int v = 0; v < NV; ++v)
@@ -188,7 +214,7 @@ __global__ __launch_bounds__(64 * WV) void kda_gdr_walk_kernel(GdrWalkParams p, 
         for (int t = HT * u; t < HT * u + HT; ++t) {
           const f32x4 cx = *reinterpret_cast<const f32x4*>(sc + Op::row4(t, g4));
 #pragma unroll
-          for (int e = 0; e < 4; ++e) X[v][t][e] = fmaf(-cx[e], X[v][t][e], V[v][t][e]);
+          for (int e = 0; e < 4; ++e) X[v][t][e] = fmaf(-cx[e], X[v][t][e], linear ? 0.f : V[v][t][e]);
         }
         x3[v][u].set(&X[v][TPU * u]);
       }
@@ -353,43 +379,142 @@ __global__ __launch_bounds__(64 * WV) void kda_gdr_walk_kernel(GdrWalkParams p, 
 #pragma unroll
       for (int u = 0; u < NUK; ++u) s2[v][u].set(&S[v][TPU * u]);
   }
-  if (p.S_T != nullptr) {
+  if (s_out != nullptr) {
 #pragma unroll
     for (int v = 0; v < NV; ++v)
 #pragma unroll
       for (int t = 0; t < CT; ++t)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) p.S_T[sbase + 16 * v + (size_t)(Op::row4(t, g4) + e) * Dv] = S[v][t][e];
+        for (int e = 0; e < 4; ++e) s_out[16 * v + (size_t)(Op::row4(t, g4) + e) * Dv] = S[v][t][e];
+  }
+}
+
+// Composes the segments' starts: start_{s+1} = M_s start_s + N_s, in place in
+// p.starts from s = 1 on.  One workgroup of 4 waves per (walk, 16 value columns): a
+// wave owns a quarter of the rows, the start goes round through LDS.  M and the start
+// are split into three bf16 terms each (float32 accuracy, 6 products).
+template <int DK>
+__global__ __launch_bounds__(256) void kda_gdr_compose_kernel(GdrWalkParams p, int Dv) {
+  constexpr int RT = DK / 64 > 0 ? DK / 64 : 1;  // row tiles of a wave
+  constexpr int NW = DK / 16 / RT;               // waves with rows
+  constexpr int NU = DK / 32, LS = DK + 4;
+  __shared__ __attribute__((aligned(16))) float st[2][16 * LS];
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, r = lane & 15, g4 = lane >> 4;
+  const int bh = blockIdx.x / (Dv / 16), v0 = blockIdx.x % (Dv / 16) * 16;
+  float* starts = p.starts + (size_t)bh * p.nseg * DK * Dv + v0;
+  const float* maps = p.maps + (size_t)bh * p.nseg * DK * DK;
+
+  auto terms = [](const float* x, bf16x8 (&t)[3]) {
+    Terms<__bf16, 3> y;
+    const f32x4 z[2] = {f32x4{x[0], x[1], x[2], x[3]}, f32x4{x[4], x[5], x[6], x[7]}};
+    y.set(z);
+#pragma unroll
+    for (int k = 0; k < 3; ++k) t[k] = y.t[k];
+  };
+  float m[RT][NU][8];
+  f32x4 nn[RT];
+  auto fetch = [&](int s) {  // this wave's rows of M_s and N_s
+#pragma unroll
+    for (int i = 0; i < RT; ++i) {
+      const int row0 = 16 * (RT * wave + i);
+#pragma unroll
+      for (int u = 0; u < NU; ++u) load8(maps + ((size_t)s * DK + row0 + r) * DK + 32 * u + 8 * g4, m[i][u]);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) nn[i][e] = starts[((size_t)(s + 1) * DK + row0 + 4 * g4 + e) * Dv + r];
+    }
+  };
+  // the start of segment 1, column by column
+  for (int i = tid; i < 16 * DK; i += 256) st[1][(i & 15) * LS + (i >> 4)] = starts[((size_t)DK + (i >> 4)) * Dv + (i & 15)];
+  if (wave < NW && p.nseg > 2) fetch(1);
+  __syncthreads();
+  for (int s = 1; s < p.nseg - 1; ++s) {
+    if (wave < NW) {
+      const float* in = st[s & 1];
+      f32x4 acc[RT];
+#pragma unroll
+      for (int i = 0; i < RT; ++i) acc[i] = nn[i];
+#pragma unroll
+      for (int u = 0; u < NU; ++u) {
+        float x[8];
+        load8(in + r * LS + 32 * u + 8 * g4, x);
+        bf16x8 b[3];
+        terms(x, b);
+#pragma unroll
+        for (int i = 0; i < RT; ++i) {
+          bf16x8 a[3];
+          terms(m[i][u], a);
+#pragma unroll
+          for (int j = 0; j < 3; ++j)
+#pragma unroll
+            for (int k = 0; k + j < 3; ++k) gmma(acc[i], a[j], b[k]);
+        }
+      }
+      if (s + 1 < p.nseg - 1) fetch(s + 1);
+#pragma unroll
+      for (int i = 0; i < RT; ++i) {
+        const int row0 = 16 * (RT * wave + i) + 4 * g4;
+        *reinterpret_cast<f32x4*>(&st[(s + 1) & 1][r * LS + row0]) = acc[i];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) starts[((size_t)(s + 1) * DK + row0 + e) * Dv + r] = acc[i][e];
+      }
+    }
+    __syncthreads();
   }
 }
 
 template <int DK, int WV, int NV, typename IO>
-static hipError_t launch_walk_t(const GdrWalkParams& p, int Dv, hipStream_t st) {
-  const unsigned grid = (unsigned)((size_t)p.s.NS * p.s.Hv * (Dv / (16 * NV * WV)));
-  if (p.ckpt != nullptr)
-    hipLaunchKernelGGL((kda_gdr_walk_kernel<DK, WV, NV, IO, false, true>), dim3(grid), dim3(64 * WV), 0, st, p,
-                       Dv);
+static hipError_t launch_pass(const GdrWalkParams& p, int Dv, hipStream_t st) {
+  const size_t per = (size_t)p.s.NS * p.s.Hv * (Dv / (16 * NV * WV));
+  const size_t segs = p.nseg > 1 ? (size_t)(p.pass == 0 ? p.nseg : p.nseg - p.pass) : 1;
+  const dim3 grid((unsigned)(per * segs)), block(64 * WV);
+  if (grid.x == 0) return hipSuccess;
+  if (p.pass != 0)
+    hipLaunchKernelGGL((kda_gdr_walk_kernel<DK, WV, NV, IO, false, false>), grid, block, 0, st, p, Dv);
+  else if (p.ckpt != nullptr)
+    hipLaunchKernelGGL((kda_gdr_walk_kernel<DK, WV, NV, IO, false, true>), grid, block, 0, st, p, Dv);
   else
-    hipLaunchKernelGGL((kda_gdr_walk_kernel<DK, WV, NV, IO, true, false>), dim3(grid), dim3(64 * WV), 0, st, p,
-                       Dv);
+    hipLaunchKernelGGL((kda_gdr_walk_kernel<DK, WV, NV, IO, true, false>), grid, block, 0, st, p, Dv);
   return hipGetLastError();
 }
 
 template <int DK, typename IO>
 static hipError_t launch_walk_d(const GdrWalkParams& p, int Dv, hipStream_t st) {
-  if (Dv == 32) return launch_walk_t<DK, 2, 1, IO>(p, Dv, st);
+  if (Dv == 32) return launch_pass<DK, 2, 1, IO>(p, Dv, st);
   if constexpr (sizeof(IO) == 2)
-    if (gdr_whole_head((long)p.s.NS * p.s.Hv, Dv)) return launch_walk_t<DK, 8, 1, IO>(p, Dv, st);
-  return launch_walk_t<DK, 4, 1, IO>(p, Dv, st);
+    if (gdr_whole_head((long)p.s.NS * p.s.Hv * (p.nseg > 1 ? p.nseg : 1), Dv))
+      return launch_pass<DK, 8, 1, IO>(p, Dv, st);
+  return launch_pass<DK, 4, 1, IO>(p, Dv, st);
+}
+
+template <typename IO>
+static hipError_t launch_walk(const GdrWalkParams& p, int Dk, int Dv, hipStream_t st) {
+  switch (Dk) {
+    case 32: return launch_walk_d<32, IO>(p, Dv, st);
+    case 64: return launch_walk_d<64, IO>(p, Dv, st);
+    case 128: return launch_walk_d<128, IO>(p, Dv, st);
+  }
+  return hipErrorInvalidValue;
 }
 
 hipError_t launch_gdr_walk(const GdrWalkParams& p, int Dk, int Dv, bool fp32, hipStream_t st) {
-  switch (Dk) {
-    case 32: return fp32 ? launch_walk_d<32, float>(p, Dv, st) : launch_walk_d<32, __bf16>(p, Dv, st);
-    case 64: return fp32 ? launch_walk_d<64, float>(p, Dv, st) : launch_walk_d<64, __bf16>(p, Dv, st);
-    case 128: return fp32 ? launch_walk_d<128, float>(p, Dv, st) : launch_walk_d<128, __bf16>(p, Dv, st);
+  auto walk = [&](const GdrWalkParams& q, int cols) {
+    return fp32 ? launch_walk<float>(q, Dk, cols, st) : launch_walk<__bf16>(q, Dk, cols, st);
+  };
+  if (p.nseg > 1) {
+    GdrWalkParams q = p;
+    q.pass = 1;
+    if (hipError_t e = walk(q, Dv); e != hipSuccess) return e;
+    q.pass = 2;
+    if (hipError_t e = walk(q, Dk); e != hipSuccess) return e;
+    const dim3 grid((unsigned)((size_t)p.s.B * p.s.Hv * (Dv / 16)));
+    switch (Dk) {
+      case 32: hipLaunchKernelGGL(kda_gdr_compose_kernel<32>, grid, dim3(256), 0, st, p, Dv); break;
+      case 64: hipLaunchKernelGGL(kda_gdr_compose_kernel<64>, grid, dim3(256), 0, st, p, Dv); break;
+      default: hipLaunchKernelGGL(kda_gdr_compose_kernel<128>, grid, dim3(256), 0, st, p, Dv); break;
+    }
+    if (hipError_t e = hipGetLastError(); e != hipSuccess) return e;
   }
-  return hipErrorInvalidValue;
+  return walk(p, Dv);
 }
 
 }  // namespace kda

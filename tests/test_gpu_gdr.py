@@ -109,6 +109,18 @@ def test_prefill_options(io):
     check_forward(d, opt, io, l2=False)
 
 
+@pytest.mark.parametrize("io", ["bf16", "fp32"])
+@pytest.mark.parametrize("shape,rate", [((1, 1100, 1, 2, 128, 128), (-8.0, -5.0)), ((2, 1601, 2, 2, 64, 32), (-9.0, 0.0)),
+                                        ((1, 2573, 1, 1, 32, 64), (-7.0, -4.0)), ((1, 1537, 1, 3, 128, 64), (-3.0, 2.0))],
+                         ids=str)
+def test_prefill_split(shape, rate, io):
+    """Few long rows, whose walks are cut into segments; the state carries far, so
+    the segments' maps count."""
+    d, opt = make(*shape, io, seed=shape[1], rate=rate)
+    check_forward(d, opt, io)
+    check_forward(dict(d, S0=None), opt, io)
+
+
 LENS = [[0, 1, 0, 70, 64, 3, 0, 129, 32, 0], [5], [0, 0, 0], [1] * 40]
 
 
