@@ -9,13 +9,36 @@
 // Tm comes from the 16 x 16 diagonal blocks by substitution, one wave each, and
 // from the blocks below them by T_ij = -T_ii sum_k A_ik T_kj, diagonal by
 // diagonal, in float32 throughout.
+//
+// It is bound by the records it writes (20 KB a chunk beside 32 KB of rows read: 3.6
+// TB/s at 64k tokens, 12 heads); one workgroup for all value heads of a key head,
+// which forms the products once, measured 10% slower at 2 heads a key head.
 #include "kda_gdr_device.h"
 #include "kda_launch.h"
 
 namespace kda {
 
+// sum of squares of 16 bytes of a row (pairs taken from the whole vector: each 32-bit
+// element cast to a pair was compiled to use element 0 four times)
+__device__ __forceinline__ float squares(const u32x4& x, __bf16) {
+  const bf16x8 v = __builtin_bit_cast(bf16x8, x);
+  const bf16x2 a = __builtin_shufflevector(v, v, 0, 1), b = __builtin_shufflevector(v, v, 2, 3);
+  const bf16x2 c = __builtin_shufflevector(v, v, 4, 5), d = __builtin_shufflevector(v, v, 6, 7);
+  float s = __builtin_amdgcn_fdot2_f32_bf16(a, a, 0.f, false);
+  s = __builtin_amdgcn_fdot2_f32_bf16(b, b, s, false);
+  s = __builtin_amdgcn_fdot2_f32_bf16(c, c, s, false);
+  return __builtin_amdgcn_fdot2_f32_bf16(d, d, s, false);
+}
+__device__ __forceinline__ float squares(const u32x4& x, float) {
+  const f32x4 y = __builtin_bit_cast(f32x4, x);
+  float s = 0.f;
+#pragma unroll
+  for (int e = 0; e < 4; ++e) s = fmaf(y[e], y[e], s);
+  return s;
+}
+
 template <int DK, typename IO, bool BWD>
-__global__ __launch_bounds__(256) void kda_gdr_prep_kernel(GdrPrepParams p) {
+__global__ __launch_bounds__(256, 3) void kda_gdr_prep_kernel(GdrPrepParams p) {
   constexpr bool F32 = sizeof(IO) == 4;
   constexpr int C = gdr_chunk(F32);
   constexpr int NTL = C / 16;                // tiles per side
@@ -27,16 +50,16 @@ __global__ __launch_bounds__(256) void kda_gdr_prep_kernel(GdrPrepParams p) {
   constexpr int LA = C + 4;                  // row stride of the float32 matrices
   constexpr int IMG = C * DK * (int)sizeof(IO);
   constexpr int MAT = C * LA * 4;
-  // Tm overwrites the k and q images once the products are done
-  constexpr int BYTES = (2 * IMG > MAT ? 2 * IMG : MAT);
+  // a and Tm overwrite the k and q images once the products are in registers
+  constexpr int BYTES = (IMG > MAT ? 2 * IMG : 2 * MAT);
   __shared__ __attribute__((aligned(16))) char lds[BYTES];
-  __shared__ __attribute__((aligned(16))) float As[C * LA];
   __shared__ __attribute__((aligned(16))) float sc[kGdrScalars][C];
   IO* ik = reinterpret_cast<IO*>(lds);
   IO* iq = reinterpret_cast<IO*>(lds + IMG);
   float* Ts = reinterpret_cast<float*>(lds);
+  float* As = Ts + C * LA;
 
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, r = lane & 15, g4 = lane >> 4;
+  const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6), r = lane & 15, g4 = lane >> 4;
   const int pos = xcd_major(blockIdx.x, gridDim.x);
   const int h = pos % p.s.Hv, row = pos / p.s.Hv;
   const int b = row % p.s.B, slot = row / p.s.B;
@@ -44,23 +67,25 @@ __global__ __launch_bounds__(256) void kda_gdr_prep_kernel(GdrPrepParams p) {
   const GdrChunk ch = gdr_chunk_at(p.s, slot, b, h, C);
   if (ch.n == 0) return;  // uniform: a slot no sequence owns
 
-  // ---- every global load first: the rows of k and q, the gates
+  // ---- every global load first: the rows of k and q (rows behind the sequence's end
+  // lie behind the buffer: zeros), the gates
   constexpr int PIECES = C * RC;             // 16-byte pieces of one image
   constexpr int NL = (PIECES + 255) / 256;
-  f32x4 raw[2][NL];
+  u32x4 raw[2][NL];
 #pragma unroll
-  for (int x = 0; x < 2; ++x)
+  for (int x = 0; x < 2; ++x) {
+    const int stride = (int)(x ? p.s.qs : p.s.ks) * (int)sizeof(IO);
+    const IO* base = (x ? static_cast<const IO*>(p.q) : static_cast<const IO*>(p.k)) +
+                     ch.tok * (x ? p.s.qs : p.s.ks) + (size_t)hk * DK;
+    const BufRes buf = make_buf(base, (unsigned)((ch.n - 1) * stride + DK * (int)sizeof(IO)));
 #pragma unroll
     for (int it = 0; it < NL; ++it) {
-      const int i = it * 256 + tid, t = i / RC, c = i % RC;
-      const IO* src = x ? static_cast<const IO*>(p.q) + (ch.tok + t) * p.s.qs
-                        : static_cast<const IO*>(p.k) + (ch.tok + t) * p.s.ks;
-      raw[x][it] = f32x4{0.f, 0.f, 0.f, 0.f};
-      if ((PIECES % 256 == 0 || i < PIECES) && t < ch.n)
-        raw[x][it] = *reinterpret_cast<const f32x4*>(src + (size_t)hk * DK + c * EPC);
+      const int i = it * 256 + tid;
+      raw[x][it] = __builtin_amdgcn_raw_buffer_load_b128(buf, i / RC * stride + i % RC * 16, 0, 0);
     }
-  // wave 0, a lane per token: the decay summed in float64, in log2 units
-  if (wave == 0) {
+  }
+  // one wave, a lane per token: the gates; the decay summed in float64, in log2 units
+  if (wave == 3) {
     float gt = 0.f, bt = 0.f;
     if (lane < ch.n && lane < C) {
       const size_t at = (size_t)(ch.tok + lane) * p.s.Hv + h;
@@ -86,15 +111,45 @@ __global__ __launch_bounds__(256) void kda_gdr_prep_kernel(GdrPrepParams p) {
     for (int it = 0; it < NL; ++it) {
       const int i = it * 256 + tid, t = i / RC, c = i % RC;
       if (PIECES % 256 != 0 && i >= PIECES) continue;
-      *reinterpret_cast<f32x4*>((x ? iq : ik) + (t * RC + GOp<IO>::template swz<RC>(t, c)) * EPC) = raw[x][it];
-      const IO* e8 = reinterpret_cast<const IO*>(&raw[x][it]);
-      float ss = 0.f;
-#pragma unroll
-      for (int e = 0; e < EPC; ++e) ss = fmaf(to_f32(e8[e]), to_f32(e8[e]), ss);
-      ss = group_sum<RC>(ss);
+      *reinterpret_cast<u32x4*>((x ? iq : ik) + (t * RC + GOp<IO>::template swz<RC>(t, c)) * EPC) = raw[x][it];
+      const float ss = group_sum<RC>(squares(raw[x][it], IO{}));
       if (c == 0) sc[x ? 4 : 3][t] = t < ch.n ? (p.l2 ? 1.0f / sqrtf(ss + p.eps) : 1.0f) : 0.f;
     }
   __syncthreads();
+
+  // ---- the raw products: wave w has row tile w.  Both are formed so that a lane holds
+  // 4 consecutive elements of a row of what is stored: k k^T by rows, q k^T by rows
+  // (forward) or by columns (backward, which reads P^T).
+  f32x4 kk[NTL], qk[NTL];
+  if (wave < NTL) {
+    Frag fw[NU], fx[NU];
+#pragma unroll
+    for (int u = 0; u < NU; ++u) {
+      fw[u] = g_row<IO, DK>(ik, 16 * wave + r, u, g4);
+      if constexpr (!BWD) fx[u] = g_row<IO, DK>(iq, 16 * wave + r, u, g4);
+    }
+#pragma unroll
+    for (int t = 0; t < NTL; ++t) {
+      kk[t] = qk[t] = f32x4{0.f, 0.f, 0.f, 0.f};
+      if (t <= wave) {
+#pragma unroll
+        for (int u = 0; u < NU; ++u) {
+          const Frag f = t == wave ? fw[u] : g_row<IO, DK>(ik, 16 * t + r, u, g4);
+          gmma(kk[t], f, fw[u]);
+          if constexpr (!BWD) gmma(qk[t], f, fx[u]);
+        }
+      }
+      if (BWD && t >= wave) {
+#pragma unroll
+        for (int u = 0; u < NU; ++u) gmma(qk[t], g_row<IO, DK>(iq, 16 * t + r, u, g4), fw[u]);
+      }
+    }
+  }
+
+  __syncthreads();  // every read of the images is done
+
+  char* rec = p.rec + ch.rec * R.bytes;
+  IO* recP = reinterpret_cast<IO*>(rec + R.p);
   if (tid < C) {
     const float rk = sc[3][tid], sq = sc[4][tid] * p.scale;
     const float gam = exp2_fast(sc[5][tid] + sc[6][tid]);
@@ -103,22 +158,10 @@ __global__ __launch_bounds__(256) void kda_gdr_prep_kernel(GdrPrepParams p) {
     sc[1][tid] = sc[7][tid] * lam * rk;
     sc[2][tid] = gam * sq;
   }
-
-  char* rec = p.rec + ch.rec * R.bytes;
-  IO* recP = reinterpret_cast<IO*>(rec + R.p);
-  // ---- a and P: wave w takes the tiles of row tile w (below it, of column tile w).
-  // Both are formed so that a lane holds 4 consecutive elements of a row of what is
-  // stored: a by rows, P by rows (forward) or by columns (backward, which reads P^T).
-  Frag fw[NU], fx[NU];  // this wave's rows of k; of q (forward: rows i) or k (columns j)
+  // ---- a and P
   if (wave < NTL) {
-#pragma unroll
-    for (int u = 0; u < NU; ++u) {
-      fw[u] = g_row<IO, DK>(ik, 16 * wave + r, u, g4);
-      if constexpr (!BWD) fx[u] = g_row<IO, DK>(iq, 16 * wave + r, u, g4);
-    }
-    // a, rows i = 16 wave + r: lanes hold columns j = 16 tj + 4 g4 ..
     const int i = 16 * wave + r;
-    const float gi = sc[5][i], li = sc[6][i], ri = sc[3][i], si = sc[4][i] * p.scale, bi = sc[7][i];
+    const float gi = sc[5][i], li = sc[6][i], ri = sc[3][i], si = sc[4][i] * p.scale, bi = sc[7][i] * ri;
 #pragma unroll
     for (int tj = 0; tj < NTL; ++tj) {
       if (tj > wave) {
@@ -127,13 +170,6 @@ __global__ __launch_bounds__(256) void kda_gdr_prep_kernel(GdrPrepParams p) {
           store4(recP + tri_slot<IO, NUC, false>(i, 16 * tj + 4 * g4, 0, 1), 0.f, 0.f, 0.f, 0.f);
         continue;
       }
-      f32x4 kk = {0.f, 0.f, 0.f, 0.f}, qk = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-      for (int u = 0; u < NU; ++u) {
-        const Frag fj = tj == wave ? fw[u] : g_row<IO, DK>(ik, 16 * tj + r, u, g4);
-        gmma(kk, fj, fw[u]);
-        if constexpr (!BWD) gmma(qk, fj, fx[u]);
-      }
       const int j = 16 * tj + 4 * g4;
       const f32x4 gj = *reinterpret_cast<const f32x4*>(&sc[5][j]), lj = *reinterpret_cast<const f32x4*>(&sc[6][j]),
                   rj = *reinterpret_cast<const f32x4*>(&sc[3][j]), bj = *reinterpret_cast<const f32x4*>(&sc[7][j]);
@@ -141,8 +177,12 @@ __global__ __launch_bounds__(256) void kda_gdr_prep_kernel(GdrPrepParams p) {
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         const float d = exp2_fast((gi - gj[e]) + (li - lj[e])) * (bj[e] * rj[e]);
-        av[e] = i > j + e ? d * ri * kk[e] : 0.f;
-        pv[e] = i >= j + e ? d * si * qk[e] : 0.f;
+        av[e] = d * ri * kk[tj][e];
+        pv[e] = d * si * qk[tj][e];
+        if (tj == wave) {
+          av[e] = i > j + e ? av[e] : 0.f;
+          pv[e] = i >= j + e ? pv[e] : 0.f;
+        }
       }
       *reinterpret_cast<f32x4*>(&As[i * LA + j]) = av;
       if constexpr (!BWD) store4(recP + tri_slot<IO, NUC, false>(i, j, 0, 1), pv[0], pv[1], pv[2], pv[3]);
@@ -150,27 +190,24 @@ __global__ __launch_bounds__(256) void kda_gdr_prep_kernel(GdrPrepParams p) {
     if constexpr (BWD) {
       // P^T, rows j = 16 wave + r: lanes hold i = 16 ti + 4 g4 ..
       const int j = i;
-      const float bj = bi * ri;
 #pragma unroll
       for (int ti = 0; ti < NTL; ++ti) {
+        const int i4 = 16 * ti + 4 * g4;
         if (ti < wave) {
           if (ti / TPU == wave / TPU)
 #pragma unroll
             for (int k = 0; k < TT; ++k)
-              store4(recP + tri_slot<IO, NUC, true>(j, 16 * ti + 4 * g4, k, TT), 0.f, 0.f, 0.f, 0.f);
+              store4(recP + tri_slot<IO, NUC, true>(j, i4, k, TT), 0.f, 0.f, 0.f, 0.f);
           continue;
         }
-        f32x4 qk = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-        for (int u = 0; u < NU; ++u) gmma(qk, g_row<IO, DK>(iq, 16 * ti + r, u, g4), fw[u]);
-        const int i4 = 16 * ti + 4 * g4;
         const f32x4 g_i = *reinterpret_cast<const f32x4*>(&sc[5][i4]), l_i = *reinterpret_cast<const f32x4*>(&sc[6][i4]),
                     s_i = *reinterpret_cast<const f32x4*>(&sc[4][i4]);
         float pv[4], lo[4];
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          const float d = exp2_fast((g_i[e] - gi) + (l_i[e] - li)) * bj;
-          pv[e] = i4 + e >= j ? d * (s_i[e] * p.scale) * qk[e] : 0.f;
+          const float d = exp2_fast((g_i[e] - gi) + (l_i[e] - li)) * bi;
+          pv[e] = d * (s_i[e] * p.scale) * qk[ti][e];
+          if (ti == wave) pv[e] = i4 + e >= j ? pv[e] : 0.f;
           lo[e] = pv[e] - to_f32(from_f32<IO>(pv[e]));
         }
         store4(recP + tri_slot<IO, NUC, true>(j, i4, 0, TT), pv[0], pv[1], pv[2], pv[3]);
@@ -188,6 +225,7 @@ __global__ __launch_bounds__(256) void kda_gdr_prep_kernel(GdrPrepParams p) {
     for (int i = 0; i < 16; ++i) x[i] = i == r ? 1.f : 0.f;
 #pragma unroll
     for (int i = 1; i < 16; ++i) {
+      if (i == 7 || i == 11 || i == 14) __builtin_amdgcn_sched_barrier(0);  // few rows of a in registers at once
 #pragma unroll
       for (int j4 = 0; j4 < i; j4 += 4) {
         const f32x4 a = *reinterpret_cast<const f32x4*>(A + i * LA + j4);
@@ -260,9 +298,9 @@ static hipError_t launch_prep_t(const GdrPrepParams& p, int Dk, bool bwd, hipStr
   if (grid == 0) return hipSuccess;
 #define KDA_GDR_PREP(D)                                                                          \
   if (bwd)                                                                                       \
-    hipLaunchKernelGGL((kda_gdr_prep_kernel<D, IO, true>), dim3(grid), dim3(256), 0, st, p);       \
+    hipLaunchKernelGGL((kda_gdr_prep_kernel<D, IO, true>), dim3(grid), dim3(256), 0, st, p);     \
   else                                                                                           \
-    hipLaunchKernelGGL((kda_gdr_prep_kernel<D, IO, false>), dim3(grid), dim3(256), 0, st, p);        \
+    hipLaunchKernelGGL((kda_gdr_prep_kernel<D, IO, false>), dim3(grid), dim3(256), 0, st, p);    \
   break
   switch (Dk) {
     case 32: KDA_GDR_PREP(32);
