@@ -430,7 +430,7 @@ struct GdrCopy {
 #pragma unroll
     for (int it = 0; it < ITERS; ++it) load(img, it, reinterpret_cast<const char*>(base), off[it], wave);
   }
-  __device__ __forceinline__ void part(char* img, const IO* base, long stride, int last, int wave) const {
+  __device__ __forceinline__ static void part(char* img, const IO* base, long stride, int last, int wave) {
 #pragma unroll
     for (int it = 0; it < ITERS; ++it)
       load(img, it, reinterpret_cast<const char*>(base), offset(it, (uint32_t)(stride * (long)sizeof(IO)), last),
