@@ -89,6 +89,15 @@ constexpr GdrSplit gdr_split(long walks, int nch, int Dv, bool fp32) {
 // Whether a walk's workgroup takes 128 value columns (8 waves) or 64 (4 waves) with
 // bf16 inputs; LDS holds one workgroup of either.
 constexpr bool gdr_whole_head(long walks, int Dv) { return Dv % 128 == 0 && walks > 128; }
+// Of walks of one length, those that would occupy at most half of the CUs at the end,
+// each a whole head: they are taken in halves of a head, on up to twice the CUs.
+constexpr int gdr_last_walks(long walks) { return walks > 256 && walks % 256 <= 128 ? (int)(walks % 256) : 0; }
+
+// Workgroups of `count` walks in nv value blocks, `share` walks with common q, k rows:
+// whole groups of them, eight at a time (gdr_walk_id).
+constexpr size_t gdr_walk_grid(long count, int share, int nv) {
+  return (size_t)((count + share - 1) / share + 7) / 8 * 8 * share * nv;
+}
 
 struct GdrPrepParams {
   GdrShape s;
@@ -128,6 +137,7 @@ struct GdrWalkParams {
   float* starts;
   float* maps;
   int pass;  // 0: outputs; 1: N; 2: M
+  int walk0, walks;  // set by the launcher: a launch's share of the walks (or segments)
 };
 
 struct GdrReverseParams {

@@ -450,14 +450,18 @@ __device__ __forceinline__ void gdr_copy_flat(char* img, const char* base, int w
   }
 }
 
-// this workgroup's walk: (sequence, value head) and value block, the blocks of a
-// walk on one XCD so that they share its q, k rows and records in L2
-__device__ __forceinline__ void gdr_walk_id(int nv, int& bh, int& vblk) {
-  const int pos = xcd_major(blockIdx.x, gridDim.x);
-  vblk = pos % nv;
-  bh = pos / nv;
+// this workgroup's walk of `count` (sequence, value head) and its value block; false: none.
+// The heads that share q, k rows (`share` of them) and their value blocks run on one
+// XCD, whose L2 serves their common rows; the groups go round the XCDs, so that a
+// long sequence's heads and a short one's are spread evenly (packed prompts of 0 to
+// 1024 tokens, 32 heads: 122 us with the walks listed XCD by XCD, 81 us as here).
+__device__ __forceinline__ bool gdr_walk_id(int nv, int share, int count, int& bh, int& vblk) {
+  const int blk = blockIdx.x, x = blk & 7, i = blk >> 3, unit = share * nv;
+  const int member = i % unit;
+  bh = (i / unit * 8 + x) * share + member / nv;
+  vblk = member % nv;
+  return bh < count;
 }
-
 // The gates of one token and head: the log-decay (a decay below e^-1000 is 0 in
 // any use, and -inf must not meet -inf in a difference; NaN passes) and beta.
 template <typename IO>

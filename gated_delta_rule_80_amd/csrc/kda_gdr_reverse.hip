@@ -44,7 +44,7 @@ __global__ __launch_bounds__(64 * WV) void kda_gdr_reverse_kernel(GdrReversePara
 
   const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6), r = lane & 15, g4 = lane >> 4;
   int bh, vblk;
-  gdr_walk_id(Dv / VB, bh, vblk);
+  if (!gdr_walk_id(Dv / VB, p.s.Hv / p.s.Hk, p.s.NS * p.s.Hv, bh, vblk)) return;  // uniform
   const int h = bh % p.s.Hv, b = bh / p.s.Hv, hk = h / (p.s.Hv / p.s.Hk);
   const GdrSpan sp = gdr_span(p.s, b, h, C);
   const int v0 = vblk * VB + 16 * NV * wave;  // this wave's value columns
@@ -335,7 +335,7 @@ __global__ __launch_bounds__(64 * WV) void kda_gdr_reverse_kernel(GdrReversePara
 
 template <int DK, int WV, int NV, typename IO>
 static hipError_t launch_reverse_t(const GdrReverseParams& p, int Dv, hipStream_t st) {
-  const unsigned grid = (unsigned)((size_t)p.s.NS * p.s.Hv * (Dv / (16 * NV * WV)));
+  const unsigned grid = (unsigned)gdr_walk_grid((long)p.s.NS * p.s.Hv, p.s.Hv / p.s.Hk, Dv / (16 * NV * WV));
   hipLaunchKernelGGL((kda_gdr_reverse_kernel<DK, WV, NV, IO>), dim3(grid), dim3(64 * WV), 0, st, p, Dv);
   return hipGetLastError();
 }

@@ -56,7 +56,8 @@ __global__ __launch_bounds__(64 * WV) void kda_gdr_walk_kernel(GdrWalkParams p, 
 
   const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6), r = lane & 15, g4 = lane >> 4;
   int bh, vblk, seg = 0;
-  gdr_walk_id(Dv / VB, bh, vblk);
+  if (!gdr_walk_id(Dv / VB, p.s.Hv / p.s.Hk, p.walks, bh, vblk)) return;  // uniform
+  bh += p.walk0;
   if (p.nseg > 1) {
     const int walks = p.s.B * p.s.Hv;
     seg = bh / walks + (p.pass == 2 ? 1 : 0);  // the first segment needs no M
@@ -390,13 +391,12 @@ __global__ __launch_bounds__(64 * WV) void kda_gdr_walk_kernel(GdrWalkParams p, 
 }
 
 // Composes the segments' starts: start_{s+1} = M_s start_s + N_s, in place in
-// p.starts from s = 1 on.  One workgroup of 4 waves per (walk, 16 value columns): a
-// wave owns a quarter of the rows, the start goes round through LDS.  M and the start
-// are split into three bf16 terms each (float32 accuracy, 6 products).
+// p.starts from s = 1 on.  One workgroup per (walk, 16 value columns): a wave owns 16
+// rows, the start goes round through LDS.  M and the start are split into three bf16
+// terms each (float32 accuracy, 6 products).  Bound by the chain of steps: reading M
+// is kept a step ahead, splitting it spread over as many waves as there are row tiles.
 template <int DK>
-__global__ __launch_bounds__(256) void kda_gdr_compose_kernel(GdrWalkParams p, int Dv) {
-  constexpr int RT = DK / 64 > 0 ? DK / 64 : 1;  // row tiles of a wave
-  constexpr int NW = DK / 16 / RT;               // waves with rows
+__global__ __launch_bounds__(4 * DK) void kda_gdr_compose_kernel(GdrWalkParams p, int Dv) {
   constexpr int NU = DK / 32, LS = DK + 4;
   __shared__ __attribute__((aligned(16))) float st[2][16 * LS];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, r = lane & 15, g4 = lane >> 4;
@@ -411,62 +411,57 @@ __global__ __launch_bounds__(256) void kda_gdr_compose_kernel(GdrWalkParams p, i
 #pragma unroll
     for (int k = 0; k < 3; ++k) t[k] = y.t[k];
   };
-  float m[RT][NU][8];
-  f32x4 nn[RT];
-  auto fetch = [&](int s) {  // this wave's rows of M_s and N_s
+  const int row0 = 16 * wave;
+  struct Rows {  // this wave's rows of M_s and N_s
+    float m[NU][8];
+    f32x4 n;
+  };
+  auto fetch = [&](int s, Rows& x) {
+    s = s < p.nseg - 1 ? s : p.nseg - 2;
 #pragma unroll
-    for (int i = 0; i < RT; ++i) {
-      const int row0 = 16 * (RT * wave + i);
+    for (int u = 0; u < NU; ++u) load8(maps + ((size_t)s * DK + row0 + r) * DK + 32 * u + 8 * g4, x.m[u]);
 #pragma unroll
-      for (int u = 0; u < NU; ++u) load8(maps + ((size_t)s * DK + row0 + r) * DK + 32 * u + 8 * g4, m[i][u]);
+    for (int e = 0; e < 4; ++e) x.n[e] = starts[((size_t)(s + 1) * DK + row0 + 4 * g4 + e) * Dv + r];
+  };
+  auto step = [&](int s, const Rows& x) {
+    const float* in = st[s & 1];
+    f32x4 acc = x.n;
 #pragma unroll
-      for (int e = 0; e < 4; ++e) nn[i][e] = starts[((size_t)(s + 1) * DK + row0 + 4 * g4 + e) * Dv + r];
+    for (int u = 0; u < NU; ++u) {
+      float y[8];
+      load8(in + r * LS + 32 * u + 8 * g4, y);
+      bf16x8 a[3], b[3];
+      terms(y, b);
+      terms(x.m[u], a);
+#pragma unroll
+      for (int j = 0; j < 3; ++j)
+#pragma unroll
+        for (int k = 0; k + j < 3; ++k) gmma(acc, a[j], b[k]);
     }
+    *reinterpret_cast<f32x4*>(&st[(s + 1) & 1][r * LS + row0 + 4 * g4]) = acc;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) starts[((size_t)(s + 1) * DK + row0 + 4 * g4 + e) * Dv + r] = acc[e];
   };
   // the start of segment 1, column by column
-  for (int i = tid; i < 16 * DK; i += 256) st[1][(i & 15) * LS + (i >> 4)] = starts[((size_t)DK + (i >> 4)) * Dv + (i & 15)];
-  if (wave < NW && p.nseg > 2) fetch(1);
-  __syncthreads();
-  for (int s = 1; s < p.nseg - 1; ++s) {
-    if (wave < NW) {
-      const float* in = st[s & 1];
-      f32x4 acc[RT];
-#pragma unroll
-      for (int i = 0; i < RT; ++i) acc[i] = nn[i];
-#pragma unroll
-      for (int u = 0; u < NU; ++u) {
-        float x[8];
-        load8(in + r * LS + 32 * u + 8 * g4, x);
-        bf16x8 b[3];
-        terms(x, b);
-#pragma unroll
-        for (int i = 0; i < RT; ++i) {
-          bf16x8 a[3];
-          terms(m[i][u], a);
-#pragma unroll
-          for (int j = 0; j < 3; ++j)
-#pragma unroll
-            for (int k = 0; k + j < 3; ++k) gmma(acc[i], a[j], b[k]);
-        }
-      }
-      if (s + 1 < p.nseg - 1) fetch(s + 1);
-#pragma unroll
-      for (int i = 0; i < RT; ++i) {
-        const int row0 = 16 * (RT * wave + i) + 4 * g4;
-        *reinterpret_cast<f32x4*>(&st[(s + 1) & 1][r * LS + row0]) = acc[i];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) starts[((size_t)(s + 1) * DK + row0 + e) * Dv + r] = acc[i][e];
-      }
-    }
-    __syncthreads();
+  for (int i = tid; i < 16 * DK; i += 4 * DK)
+    st[1][(i & 15) * LS + (i >> 4)] = starts[((size_t)DK + (i >> 4)) * Dv + (i & 15)];
+  Rows x, y;  // of this step and the next, whose reads are under way meanwhile
+  if (p.nseg > 2) fetch(1, x);
+  lds_barrier();
+  for (int s = 1; s < p.nseg - 1; s += 2) {
+    fetch(s + 1, y);
+    step(s, x);
+    lds_barrier();
+    if (s + 1 == p.nseg - 1) break;  // uniform
+    fetch(s + 2, x);
+    step(s + 1, y);
+    lds_barrier();
   }
 }
 
 template <int DK, int WV, int NV, typename IO>
 static hipError_t launch_pass(const GdrWalkParams& p, int Dv, hipStream_t st) {
-  const size_t per = (size_t)p.s.NS * p.s.Hv * (Dv / (16 * NV * WV));
-  const size_t segs = p.nseg > 1 ? (size_t)(p.pass == 0 ? p.nseg : p.nseg - p.pass) : 1;
-  const dim3 grid((unsigned)(per * segs)), block(64 * WV);
+  const dim3 grid((unsigned)gdr_walk_grid(p.walks, p.s.Hv / p.s.Hk, Dv / (16 * NV * WV))), block(64 * WV);
   if (grid.x == 0) return hipSuccess;
   if (p.pass != 0)
     hipLaunchKernelGGL((kda_gdr_walk_kernel<DK, WV, NV, IO, false, false>), grid, block, 0, st, p, Dv);
@@ -478,11 +473,21 @@ static hipError_t launch_pass(const GdrWalkParams& p, int Dv, hipStream_t st) {
 }
 
 template <int DK, typename IO>
-static hipError_t launch_walk_d(const GdrWalkParams& p, int Dv, hipStream_t st) {
+static hipError_t launch_walk_d(const GdrWalkParams& all, int Dv, hipStream_t st) {
+  GdrWalkParams p = all;
+  p.walk0 = 0;
+  p.walks = p.s.NS * p.s.Hv * (p.nseg > 1 ? (p.pass == 0 ? p.nseg : p.nseg - p.pass) : 1);
   if (Dv == 32) return launch_pass<DK, 2, 1, IO>(p, Dv, st);
   if constexpr (sizeof(IO) == 2)
-    if (gdr_whole_head((long)p.s.NS * p.s.Hv * (p.nseg > 1 ? p.nseg : 1), Dv))
-      return launch_pass<DK, 8, 1, IO>(p, Dv, st);
+    if (gdr_whole_head((long)p.s.NS * p.s.Hv * (p.nseg > 1 ? p.nseg : 1), Dv)) {
+      GdrWalkParams whole = p;
+      const int rest = p.nseg > 1 || p.s.seqs.bounds != nullptr ? 0 : gdr_last_walks(p.walks);
+      whole.walks -= rest;
+      if (hipError_t e = launch_pass<DK, 8, 1, IO>(whole, Dv, st); e != hipSuccess || rest == 0) return e;
+      whole.walk0 = whole.walks;
+      whole.walks = rest;
+      return launch_pass<DK, 4, 1, IO>(whole, Dv, st);
+    }
   return launch_pass<DK, 4, 1, IO>(p, Dv, st);
 }
 
@@ -508,9 +513,9 @@ hipError_t launch_gdr_walk(const GdrWalkParams& p, int Dk, int Dv, bool fp32, hi
     if (hipError_t e = walk(q, Dk); e != hipSuccess) return e;
     const dim3 grid((unsigned)((size_t)p.s.B * p.s.Hv * (Dv / 16)));
     switch (Dk) {
-      case 32: hipLaunchKernelGGL(kda_gdr_compose_kernel<32>, grid, dim3(256), 0, st, p, Dv); break;
+      case 32: hipLaunchKernelGGL(kda_gdr_compose_kernel<32>, grid, dim3(128), 0, st, p, Dv); break;
       case 64: hipLaunchKernelGGL(kda_gdr_compose_kernel<64>, grid, dim3(256), 0, st, p, Dv); break;
-      default: hipLaunchKernelGGL(kda_gdr_compose_kernel<128>, grid, dim3(256), 0, st, p, Dv); break;
+      default: hipLaunchKernelGGL(kda_gdr_compose_kernel<128>, grid, dim3(512), 0, st, p, Dv); break;
     }
     if (hipError_t e = hipGetLastError(); e != hipSuccess) return e;
   }

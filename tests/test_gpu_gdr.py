@@ -121,6 +121,15 @@ def test_prefill_split(shape, rate, io):
     check_forward(dict(d, S0=None), opt, io)
 
 
+@pytest.mark.parametrize("io", ["bf16", "fp32"])
+@pytest.mark.parametrize("B", [5, 8, 9])
+def test_many_walks(B, io):
+    """More walks than the card holds workgroups, also a few more than that many."""
+    d, opt = make(B, 70, 8, 32, 32, 128, io, seed=B)
+    check_forward(d, opt, io)
+    check_backward(d, opt, io)
+
+
 LENS = [[0, 1, 0, 70, 64, 3, 0, 129, 32, 0], [5], [0, 0, 0], [1] * 40]
 
 
