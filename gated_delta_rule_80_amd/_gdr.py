@@ -109,6 +109,8 @@ def _rows(t, name, shape, dtype, device):
             raise ValueError(f"{name}: rows of the batch must follow one another")
     if lead.numel() == 1:
         step = 0
+    elif step < shape[-2] * shape[-1]:  # an expanded view, say
+        raise ValueError(f"{name}: the rows of two tokens overlap")
     return t.data_ptr(), step
 
 
@@ -126,30 +128,32 @@ def _handle(stream, device):
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else stream
 
 
-def _used(stream, *tensors):
-    """Tensors made here, in a call on the caller's own stream: torch keeps their
-    memory until that stream is done with them."""
-    if isinstance(stream, torch.cuda.Stream):
-        for t in tensors:
-            if t is not None:
-                t.record_stream(stream)
-
-
-def _after_fill(stream, device):
-    """Has the caller's stream wait for fills made here on the current one."""
-    if isinstance(stream, torch.cuda.Stream):
-        stream.wait_stream(torch.cuda.current_stream(device))
+def _made(stream, device, *tensors):
+    """Tensors made here on the current stream for a call on the caller's own: that
+    stream waits for what the current one still does (with their memory, or filling
+    them), and torch keeps the memory until that stream is done with it."""
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(stream, device=device) if stream else torch.cuda.default_stream(device)
+    current = torch.cuda.current_stream(device)
+    if stream == current:
+        return
+    stream.wait_stream(current)
+    for t in tensors:
+        if t is not None:
+            t.record_stream(stream)
 
 
 def _scratch(need, device, stream, own):
     """(address, bytes) of the workspace, and what keeps it."""
     if own is not None:
+        if own.device != device:
+            raise ValueError(f"workspace is on {own.device}, expected {device}")
         return (_lib._ptr(own), own.numel() * own.element_size()), own
     if need == 0:
         return (None, 0), None
     ws = torch.empty(need, dtype=torch.uint8, device=device)
     if stream is not None:
-        _used(stream, ws)
+        _made(stream, device, ws)
     return (ws.data_ptr(), need), ws
 
 
@@ -166,6 +170,12 @@ def _list(t, name, device):
     return _lib._ptr(t)
 
 
+def _sequences(cu_seqlens):
+    if cu_seqlens.numel() < 2:
+        raise ValueError("cu_seqlens needs an offset before and one after every sequence")
+    return cu_seqlens.numel() - 1
+
+
 # ------------------------------------------------------------------ prefill
 def gdr_args(q, k, v, g, beta, S0=None, o=None, S_T=None, *, scale=1.0, l2norm_qk=True, eps=1e-6,
              A_log=None, dt_bias=None, beta_logits=False, cu_seqlens=None) -> GdrArgs:
@@ -177,7 +187,7 @@ def gdr_args(q, k, v, g, beta, S0=None, o=None, S_T=None, *, scale=1.0, l2norm_q
     gates = (B, T, Hv)
     cu, n, NS = None, 0, B
     if cu_seqlens is not None:
-        cu, NS = _list(cu_seqlens, "cu_seqlens", dev), cu_seqlens.numel() - 1
+        cu, NS = _list(cu_seqlens, "cu_seqlens", dev), _sequences(cu_seqlens)
         n = NS
     state = (NS, Hv, Dk, Dv)
     pq, sq = _rows(q, "q", qs, io, dev)
@@ -227,12 +237,12 @@ def kda_gdr_prefill(q, k, v, g, beta, S0=None, *, scale=1.0, l2norm_qk=True, eps
     if o is None:
         o = torch.empty(v.shape, dtype=q.dtype, device=dev)
         if stream is not None:
-            _used(stream, o)
+            _made(stream, dev, o)
     if S_T is None:
-        NS = q.shape[0] if cu_seqlens is None else cu_seqlens.numel() - 1
+        NS = q.shape[0] if cu_seqlens is None else _sequences(cu_seqlens)
         S_T = torch.empty(NS, v.shape[2], q.shape[3], v.shape[3], dtype=torch.float32, device=dev)
         if stream is not None:
-            _used(stream, S_T)
+            _made(stream, dev, S_T)
     a = ctypes.byref(gdr_args(q, k, v, g, beta, S0, o, S_T, scale=scale, l2norm_qk=l2norm_qk, eps=eps,
                               A_log=A_log, dt_bias=dt_bias, beta_logits=beta_logits, cu_seqlens=cu_seqlens))
     lib = _lib.load()
@@ -283,7 +293,7 @@ def kda_gdr_prefill_backward(q, k, v, g, beta, S0=None, *, do, dS_T=None, scale=
     dev, io = q.device, q.dtype
     B, T, Hk, Dk = q.shape
     Hv, Dv = v.shape[2:]
-    NS = B if cu_seqlens is None else cu_seqlens.numel() - 1
+    NS = B if cu_seqlens is None else _sequences(cu_seqlens)
     fwd = gdr_args(q, k, v, g, beta, S0, None, None, scale=scale, l2norm_qk=l2norm_qk, eps=eps, A_log=A_log,
                    dt_bias=dt_bias, beta_logits=beta_logits, cu_seqlens=cu_seqlens)
     if cu_seqlens is None:
@@ -298,9 +308,7 @@ def kda_gdr_prefill_backward(q, k, v, g, beta, S0=None, *, do, dS_T=None, scale=
         grads["dA_log"] = torch.empty(Hv, dtype=torch.float32, device=dev)
         grads["ddt_bias"] = torch.empty(Hv, dtype=torch.float32, device=dev)
     if stream is not None:
-        if cu_seqlens is not None:
-            _after_fill(stream, dev)
-        _used(stream, *grads.values())
+        _made(stream, dev, *grads.values())
     a = GdrBackwardArgs(fwd, _dense(do, "do", v.shape, io, dev),
                         _dense(dS_T, "dS_T", (NS, Hv, Dk, Dv), torch.float32, dev),
                         *(_lib._ptr(grads.get(n)) for n in _GRADS))
@@ -361,8 +369,7 @@ def kda_gdr_decode(q, k, v, g, beta, S, slots=None, *, scale=1.0, l2norm_qk=True
     if o is None:
         o = (torch.empty if slots is None else torch.zeros)(v.shape, dtype=q.dtype, device=dev)
         if stream is not None:
-            _used(stream, o)
-            _after_fill(stream, dev)
+            _made(stream, dev, o)
     a = gdr_decode_args(q, k, v, g, beta, S, slots, o, scale=scale, l2norm_qk=l2norm_qk, eps=eps, A_log=A_log,
                         dt_bias=dt_bias, beta_logits=beta_logits)
     status = _lib.load().kda_gdr_decode(ctypes.byref(a), _handle(stream, dev))
@@ -382,6 +389,8 @@ def pages_pool(pool) -> PagesPool:
     if not pool.is_contiguous():
         if not pool[0, 0].is_contiguous() or (shape[1] > 1 and pool.stride(1) != page):
             raise ValueError("the pages of a layer must be dense")
+        if shape[0] > 1 and pool.stride(0) < shape[1] * page:
+            raise ValueError("two layers overlap")
         layer = pool.stride(0) * es if shape[0] > 1 else 0
     return PagesPool(pool.data_ptr(), layer, page * es, shape[0], shape[1])
 
@@ -404,11 +413,11 @@ def kda_pages_fork(pool, refs, src, *, refs_out=None, dst=None, workspace=None, 
     if refs_out is None:
         refs_out = torch.empty(pages, dtype=i32, device=dev)
         if stream is not None:
-            _used(stream, refs_out)
+            _made(stream, dev, refs_out)
     if dst is None:
         dst = torch.empty(n, dtype=i32, device=dev)
         if stream is not None:
-            _used(stream, dst)
+            _made(stream, dev, dst)
     r, lib = ctypes.byref(p), _lib.load()
     ws, keep = _scratch(lib.kda_pages_workspace_bytes(r, n), dev, stream, workspace)
     _lib._check(lib.kda_pages_fork(r, _dense(refs, "refs", pages, i32, dev),
@@ -429,7 +438,7 @@ def kda_pages_free(refs, pages, *, refs_out=None, stream=None):
     if refs_out is None:
         refs_out = torch.empty(shape, dtype=i32, device=dev)
         if stream is not None:
-            _used(stream, refs_out)
+            _made(stream, dev, refs_out)
     _lib._check(_lib.load().kda_pages_free(_dense(refs, "refs", shape, i32, dev),
                                            _dense(refs_out, "refs_out", shape, i32, dev), shape[0],
                                            _list(pages, "pages", dev), pages.numel(), _handle(stream, dev)),
@@ -463,7 +472,7 @@ def kda_pages_compact(pool, refs, table=None, *, refs_out=None, new_id=None, tab
     else:
         table_out = None
     if stream is not None:
-        _used(stream, refs_out, new_id, n_used, table_out)
+        _made(stream, dev, refs_out, new_id, n_used, table_out)
     r, lib = ctypes.byref(p), _lib.load()
     ws, keep = _scratch(lib.kda_pages_workspace_bytes(r, 0), dev, stream, workspace)
     _lib._check(lib.kda_pages_compact(
@@ -492,7 +501,7 @@ def kda_pages_copy(src_pool, dst_pool, src, dst, *, done=None, workspace=None, s
     if done is None:
         done = torch.empty(n, dtype=torch.int32, device=dev)
         if stream is not None:
-            _used(stream, done)
+            _made(stream, dev, done)
     lib = _lib.load()
     ws, keep = _scratch(lib.kda_pages_workspace_bytes(ctypes.byref(pd), n), dev, stream, workspace)
     _lib._check(lib.kda_pages_copy(ctypes.byref(ps), ctypes.byref(pd), _list(src, "src", dev), _list(dst, "dst", dev),

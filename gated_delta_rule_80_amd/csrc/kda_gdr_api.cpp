@@ -41,6 +41,8 @@ bool stride_ok(int64_t stride, size_t row, size_t es) {
          (stride == 0 || (stride >= (int64_t)row && (size_t)stride * es % 16 == 0 && stride <= (int64_t(1) << 23)));
 }
 
+constexpr size_t kGdrMaxGroups = (size_t(1) << 23) - 1;
+
 struct GdrSizes {
   size_t q, k, v, o, gates, state, cu;  // bytes
   int NS, NT;
@@ -66,9 +68,11 @@ kda_status gdr_sizes(const kda_gdr_args* a, GdrSizes& s) {
   const long slots = gdr_packed(a) && a->T > 0 ? nt + a->n_seqs : nt;
   if (slots > 0x7fffffffL) return KDA_ERR_SHAPE;
   s.NT = (int)slots;
+  // a launch holds less than 2^32 threads, a workgroup up to 512 of them: one per
+  // chunk and head, and one per sequence and head (rounded up, gdr_walk_grid)
   size_t wgs;
-  if (!mul_ok(wgs, {(size_t)a->B, (size_t)a->Hv, (size_t)(s.NT > 0 ? s.NT : 1)}) || wgs > 0x7fffffffu ||
-      !mul_ok(wgs, {(size_t)s.NS, (size_t)a->Hv, 4}) || wgs > 0x7fffffffu)
+  if (!mul_ok(wgs, {(size_t)a->B, (size_t)a->Hv, (size_t)(s.NT > 0 ? s.NT : 1)}) || wgs > kGdrMaxGroups ||
+      !mul_ok(wgs, {(size_t)s.NS + 8, (size_t)a->Hv}) || wgs > kGdrMaxGroups)
     return KDA_ERR_SHAPE;
   return KDA_OK;
 }
@@ -392,7 +396,7 @@ kda_status kda_validate_gdr_decode(const kda_gdr_decode_args* a) {
   if (!rows_bytes(qb, n, rk, a->q_stride, es) || !rows_bytes(kb, n, rk, a->k_stride, es) ||
       !rows_bytes(vb, n, rv, a->v_stride, es) || !mul_ok(ob, {n, rv, es}) || !mul_ok(gb, {n, (size_t)a->Hv, es}) ||
       !mul_ok(sb, {(size_t)a->n_slots, (size_t)a->Hv, (size_t)a->Dk, (size_t)a->Dv, 4}) ||
-      !mul_ok(wgs, {n, (size_t)a->Hv}) || wgs > 0x7fffffffu)
+      !mul_ok(wgs, {n, (size_t)a->Hv}) || wgs > kGdrMaxGroups)
     return KDA_ERR_SHAPE;
   if ((a->A_log == nullptr) != (a->dt_bias == nullptr)) return KDA_ERR_NULL;
   if (!a->S || (a->N > 0 && (!a->q || !a->k || !a->v || !a->g || !a->beta || !a->o))) return KDA_ERR_NULL;

@@ -389,11 +389,13 @@ kda_status kda_prefill_backward_saved(const kda_backward_args* a, void* ws, size
  * Layouts: q, k [B][T][Hk][Dk]; v, o [B][T][Hv][Dv]; g, beta [B][T][Hv];
  * S0, S_T [B][Hv][Dk][Dv] float32.  q, k, v may be parts of wider rows: q_stride,
  * k_stride, v_stride are the elements between two tokens (0: packed rows; else at
- * least the row, at most 2^23, and a multiple of 16 bytes); q, k, v may overlap one another, so
- * one fused projection [B][T][row] serves all three.
+ * least the row, at most 2^23, and a multiple of 16 bytes); q, k, v may overlap one
+ * another, so one fused projection [B][T][row] serves all three.
  * Packed sequences: cu_seqlens as in kda_prefill (B = 1, offsets clamped; tokens
  * outside every sequence are left as they were in o and in the gradients).
- * Supported: Dk and Dv in {32, 64, 128}.  The chunk length is the library's own.
+ * Supported: Dk and Dv in {32, 64, 128}; fewer than 2^23 chunks (64 tokens with
+ * bf16, 32 with fp32 inputs; a packed sequence ends with one of its own) over all
+ * heads, and as many sequences.  The chunk length is the library's own.
  */
 typedef struct kda_gdr_args {
   int32_t B, T, Hk, Hv, Dk, Dv;
