@@ -38,7 +38,7 @@ __device__ __forceinline__ float squares(const u32x4& x, float) {
 }
 
 template <int DK, typename IO, bool BWD>
-__global__ __launch_bounds__(256, 3) void kda_gdr_prep_kernel(GdrPrepParams p) {
+__global__ __launch_bounds__(256, 4) void kda_gdr_prep_kernel(GdrPrepParams p) {
   constexpr bool F32 = sizeof(IO) == 4;
   constexpr int C = gdr_chunk(F32);
   constexpr int NTL = C / 16;                // tiles per side
@@ -219,16 +219,18 @@ __global__ __launch_bounds__(256, 3) void kda_gdr_prep_kernel(GdrPrepParams p) {
 
   // ---- Tm: diagonal blocks, lane = column (the 4 lane groups do the same)
   if (wave < NTL) {
-    const float* A = As + (16 * wave) * LA + 16 * wave;
+    int at = (16 * wave) * LA + 16 * wave;
     float x[16];
 #pragma unroll
     for (int i = 0; i < 16; ++i) x[i] = i == r ? 1.f : 0.f;
 #pragma unroll
     for (int i = 1; i < 16; ++i) {
-      if (i == 7 || i == 11 || i == 14) __builtin_amdgcn_sched_barrier(0);  // few rows of a in registers at once
+      // the next rows of a are addressed after these: all 15 at once would take 120
+      // registers and a workgroup's place on the CU
+      if (i == 7 || i == 10 || i == 12 || i == 14) asm volatile("" : "+v"(at), "+v"(x[i - 1]));
 #pragma unroll
       for (int j4 = 0; j4 < i; j4 += 4) {
-        const f32x4 a = *reinterpret_cast<const f32x4*>(A + i * LA + j4);
+        const f32x4 a = *reinterpret_cast<const f32x4*>(As + at + i * LA + j4);
 #pragma unroll
         for (int e = 0; e < 4; ++e)
           if (j4 + e < i) x[i] = fmaf(-a[e], x[j4 + e], x[i]);
