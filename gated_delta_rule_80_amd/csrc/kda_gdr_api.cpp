@@ -69,10 +69,10 @@ kda_status gdr_sizes(const kda_gdr_args* a, GdrSizes& s) {
   if (slots > 0x7fffffffL) return KDA_ERR_SHAPE;
   s.NT = (int)slots;
   // a launch holds less than 2^32 threads, a workgroup up to 512 of them: one per
-  // chunk and head, and one per sequence and head (rounded up, gdr_walk_grid)
+  // chunk and head, and up to two per sequence and head (rounded up, gdr_walk_grid)
   size_t wgs;
   if (!mul_ok(wgs, {(size_t)a->B, (size_t)a->Hv, (size_t)(s.NT > 0 ? s.NT : 1)}) || wgs > kGdrMaxGroups ||
-      !mul_ok(wgs, {(size_t)s.NS + 8, (size_t)a->Hv}) || wgs > kGdrMaxGroups)
+      !mul_ok(wgs, {(size_t)s.NS + 8, (size_t)a->Hv, 2}) || wgs > kGdrMaxGroups)
     return KDA_ERR_SHAPE;
   return KDA_OK;
 }
@@ -344,7 +344,6 @@ kda_status kda_gdr_prefill_backward(const kda_gdr_backward_args* a, void* ws, si
   p.S0 = f->S0;
   p.y = base + w.y;
   p.ckpt = base + w.ckS;
-  if (kda_status e = hip_status(launch_gdr_walk(p, f->Dk, f->Dv, fp32, st)); e != KDA_OK) return e;
   GdrReverseParams rv{};
   rv.s = g;
   rv.q = f->q; rv.k = f->k;
@@ -352,7 +351,7 @@ kda_status kda_gdr_prefill_backward(const kda_gdr_backward_args* a, void* ws, si
   rv.dO = a->dO; rv.dS_T = a->dS_T; rv.dS0 = a->dS0;
   rv.dv = a->dv;
   rv.ckpt = base + w.ckdS;
-  if (kda_status e = hip_status(launch_gdr_reverse(rv, f->Dk, f->Dv, fp32, st)); e != KDA_OK) return e;
+  if (kda_status e = hip_status(launch_gdr_two_walks(rv, p, f->Dk, f->Dv, fp32, st)); e != KDA_OK) return e;
   GdrGradParams d{};
   d.s = g;
   d.q = f->q; d.k = f->k;

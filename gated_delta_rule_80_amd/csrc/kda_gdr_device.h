@@ -455,8 +455,8 @@ __device__ __forceinline__ void gdr_copy_flat(char* img, const char* base, int w
 // XCD, whose L2 serves their common rows; the groups go round the XCDs, so that a
 // long sequence's heads and a short one's are spread evenly (packed prompts of 0 to
 // 1024 tokens, 32 heads: 122 us with the walks listed XCD by XCD, 81 us as here).
-__device__ __forceinline__ bool gdr_walk_id(int nv, int share, int count, int& bh, int& vblk) {
-  const int blk = blockIdx.x, x = blk & 7, i = blk >> 3, unit = share * nv;
+__device__ __forceinline__ bool gdr_walk_id(int blk, int nv, int share, int count, int& bh, int& vblk) {
+  const int x = blk & 7, i = blk >> 3, unit = share * nv;
   const int member = i % unit;
   bh = (i / unit * 8 + x) * share + member / nv;
   vblk = member % nv;

@@ -8,8 +8,11 @@
 // dS0 leaves in float32, so the operands on its path carry 3 bf16 terms (dY, co dO,
 // cx dX) or 2 (dS, Tm, P), as in the forward.  dS at each chunk's end is kept for
 // the gradient kernel in the element type.
-#include "kda_gdr_device.h"
-#include "kda_launch.h"
+//
+// It reads nothing of the forward walk (S, Y come in with the gradient kernel only), so
+// both run in one launch, the reverse ones first: where the sequences are few or unlike,
+// neither fills the card.
+#include "kda_gdr_walk.h"
 
 namespace kda {
 
@@ -29,7 +32,7 @@ struct GdrReverseLds {
 };
 
 template <int DK, int WV, int NV, typename IO>
-__global__ __launch_bounds__(64 * WV) void kda_gdr_reverse_kernel(GdrReverseParams p, int Dv) {
+__device__ __forceinline__ void gdr_reverse(const GdrReverseParams& p, int Dv, int blk, char* lds) {
   using L = GdrReverseLds<DK, WV, NV, IO>;
   using Op = GOp<IO>;
   using Frag = typename Op::Frag;
@@ -40,11 +43,9 @@ __global__ __launch_bounds__(64 * WV) void kda_gdr_reverse_kernel(GdrReversePara
   constexpr int TPU = Op::TPU, TT = L::TT, ES = L::ES;
   constexpr GdrRecord R = gdr_record(F32, true);
   constexpr int NSTORE = NV * (F32 ? 4 : 1) * (CT + TL);  // stores of a chunk
-  __shared__ __attribute__((aligned(16))) char lds[2 * L::BYTES];
-
   const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6), r = lane & 15, g4 = lane >> 4;
   int bh, vblk;
-  if (!gdr_walk_id(Dv / VB, p.s.Hv / p.s.Hk, p.s.NS * p.s.Hv, bh, vblk)) return;  // uniform
+  if (!gdr_walk_id(blk, Dv / VB, p.s.Hv / p.s.Hk, p.s.NS * p.s.Hv, bh, vblk)) return;  // uniform
   const int h = bh % p.s.Hv, b = bh / p.s.Hv, hk = h / (p.s.Hv / p.s.Hk);
   const GdrSpan sp = gdr_span(p.s, b, h, C);
   const int v0 = vblk * VB + 16 * NV * wave;  // this wave's value columns
@@ -334,25 +335,43 @@ __global__ __launch_bounds__(64 * WV) void kda_gdr_reverse_kernel(GdrReversePara
 }
 
 template <int DK, int WV, int NV, typename IO>
-static hipError_t launch_reverse_t(const GdrReverseParams& p, int Dv, hipStream_t st) {
-  const unsigned grid = (unsigned)gdr_walk_grid((long)p.s.NS * p.s.Hv, p.s.Hv / p.s.Hk, Dv / (16 * NV * WV));
-  hipLaunchKernelGGL((kda_gdr_reverse_kernel<DK, WV, NV, IO>), dim3(grid), dim3(64 * WV), 0, st, p, Dv);
+__global__ __launch_bounds__(64 * WV) void kda_gdr_two_walks_kernel(GdrReverseParams r, GdrWalkParams w, int Dv,
+                                                                    int half) {
+  constexpr int A = GdrReverseLds<DK, WV, NV, IO>::BYTES, B = GdrWalkLds<DK, WV, NV, IO, false>::BYTES;
+  __shared__ __attribute__((aligned(16))) char lds[2 * (A > B ? A : B)];
+  if ((int)blockIdx.x < half)
+    gdr_reverse<DK, WV, NV, IO>(r, Dv, blockIdx.x, lds);
+  else
+    gdr_walk<DK, WV, NV, IO, false, true>(w, Dv, blockIdx.x - half, lds);
+}
+
+template <int DK, int WV, int NV, typename IO>
+static hipError_t launch_two_t(const GdrReverseParams& r, const GdrWalkParams& w, int Dv, hipStream_t st) {
+  // half: a multiple of 8, so that both roles keep their groups on one XCD
+  const size_t half = gdr_walk_grid(w.walks, r.s.Hv / r.s.Hk, Dv / (16 * NV * WV));
+  hipLaunchKernelGGL((kda_gdr_two_walks_kernel<DK, WV, NV, IO>), dim3((unsigned)(2 * half)), dim3(64 * WV), 0, st, r,
+                     w, Dv, (int)half);
   return hipGetLastError();
 }
 
 template <int DK, typename IO>
-static hipError_t launch_reverse_w(const GdrReverseParams& p, int Dv, hipStream_t st) {
-  if (Dv == 32) return launch_reverse_t<DK, 2, 1, IO>(p, Dv, st);
+static hipError_t launch_two_w(const GdrReverseParams& r, const GdrWalkParams& all, int Dv, hipStream_t st) {
+  GdrWalkParams w = all;
+  w.nseg = 1;
+  w.pass = w.walk0 = 0;
+  w.walks = r.s.NS * r.s.Hv;
+  if (Dv == 32) return launch_two_t<DK, 2, 1, IO>(r, w, Dv, st);
   if constexpr (sizeof(IO) == 2)
-    if (gdr_whole_head((long)p.s.NS * p.s.Hv, Dv)) return launch_reverse_t<DK, 8, 1, IO>(p, Dv, st);
-  return launch_reverse_t<DK, 4, 1, IO>(p, Dv, st);
+    if (gdr_whole_head(2l * w.walks, Dv)) return launch_two_t<DK, 8, 1, IO>(r, w, Dv, st);
+  return launch_two_t<DK, 4, 1, IO>(r, w, Dv, st);
 }
 
-hipError_t launch_gdr_reverse(const GdrReverseParams& p, int Dk, int Dv, bool fp32, hipStream_t st) {
+hipError_t launch_gdr_two_walks(const GdrReverseParams& r, const GdrWalkParams& w, int Dk, int Dv, bool fp32,
+                                hipStream_t st) {
   switch (Dk) {
-    case 32: return fp32 ? launch_reverse_w<32, float>(p, Dv, st) : launch_reverse_w<32, __bf16>(p, Dv, st);
-    case 64: return fp32 ? launch_reverse_w<64, float>(p, Dv, st) : launch_reverse_w<64, __bf16>(p, Dv, st);
-    case 128: return fp32 ? launch_reverse_w<128, float>(p, Dv, st) : launch_reverse_w<128, __bf16>(p, Dv, st);
+    case 32: return fp32 ? launch_two_w<32, float>(r, w, Dv, st) : launch_two_w<32, __bf16>(r, w, Dv, st);
+    case 64: return fp32 ? launch_two_w<64, float>(r, w, Dv, st) : launch_two_w<64, __bf16>(r, w, Dv, st);
+    case 128: return fp32 ? launch_two_w<128, float>(r, w, Dv, st) : launch_two_w<128, __bf16>(r, w, Dv, st);
   }
   return hipErrorInvalidValue;
 }

@@ -395,7 +395,7 @@ kda_status kda_prefill_backward_saved(const kda_backward_args* a, void* ws, size
  * outside every sequence are left as they were in o and in the gradients).
  * Supported: Dk and Dv in {32, 64, 128}; fewer than 2^23 chunks (64 tokens with
  * bf16, 32 with fp32 inputs; a packed sequence ends with one of its own) over all
- * heads, and as many sequences.  The chunk length is the library's own.
+ * heads, and half as many sequences.  The chunk length is the library's own.
  */
 typedef struct kda_gdr_args {
   int32_t B, T, Hk, Hv, Dk, Dv;
