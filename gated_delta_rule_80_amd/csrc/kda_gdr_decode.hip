@@ -30,12 +30,9 @@ __global__ __launch_bounds__(256) void kda_gdr_decode_kernel(GdrDecodeParams p) 
   if (slot < 0 || slot >= p.n_slots) return;  // uniform: a padding row
   float* S = p.S + ((size_t)slot * p.Hv + h) * DK * DV;
 
-  // the state's loads first; nothing below delays them
-  f32x4 st[R];
-#pragma unroll
-  for (int i = 0; i < R; ++i)
-    st[i] = __builtin_nontemporal_load(reinterpret_cast<const f32x4*>(S + (size_t)(cg * R + i) * DV) + vg);
-
+  // The rows of this slot.  A row that is not its slot's first leaves before it reads
+  // the state: with two rows a slot, reading first cost 630 us where this takes 500-545 (240
+  // slots of 96 heads, 128 x 128).
   int nxt = 0x7fffffff;  // the slot's next row after this one
   if (p.slots != nullptr) {
     if (tid == 0) {
@@ -52,6 +49,10 @@ __global__ __launch_bounds__(256) void kda_gdr_decode_kernel(GdrDecodeParams p) 
     if (before) return;  // uniform: an earlier row's workgroup does this one
     nxt = next;
   }
+  f32x4 st[R];
+#pragma unroll
+  for (int i = 0; i < R; ++i)
+    st[i] = __builtin_nontemporal_load(reinterpret_cast<const f32x4*>(S + (size_t)(cg * R + i) * DV) + vg);
 
   while (true) {
     // ---- the token: q, k rows with their sums, v, gates
