@@ -72,7 +72,8 @@ struct GdrShape {
 // It triples the work of a chunk (two maps, then the outputs) for nseg times the
 // parallelism, so it pays from 6 segments on, while workgroups stay within the 256
 // CUs; segments of at least 4 chunks keep the composition (about 1 us a segment)
-// below the walks.  Measured at 64k tokens, 12 heads, D = 128, bf16: 2.88 ms unsplit.
+// below the walks.  Measured at 64k tokens, 12 heads, D = 128, bf16 (the whole call):
+// 0.79 ms in 21 segments, 2.88 ms unsplit.
 struct GdrSplit {
   int nseg, seg_len;
 };
@@ -87,10 +88,13 @@ constexpr GdrSplit gdr_split(long walks, int nch, int Dv, bool fp32) {
 }
 
 // Whether a walk's workgroup takes 128 value columns (8 waves) or 64 (4 waves) with
-// bf16 inputs; LDS holds one workgroup of either.
+// bf16 inputs; LDS holds one workgroup of either.  A chunk takes 5.2 and 3.3 us
+// (kda_gdr_walk.h): up to 128 walks the halves find a CU each and are the faster, more
+// walks' halves take two turns, 6.6 us.
 constexpr bool gdr_whole_head(long walks, int Dv) { return Dv % 128 == 0 && walks > 128; }
 // Of walks of one length, those that would occupy at most half of the CUs at the end,
-// each a whole head: they are taken in halves of a head, on up to twice the CUs.
+// each a whole head: they are taken in halves of a head, on up to twice the CUs (384
+// walks of 128 chunks: 1280 us as two turns of whole heads, 1090 us so).
 constexpr int gdr_last_walks(long walks) { return walks > 256 && walks % 256 <= 128 ? (int)(walks % 256) : 0; }
 
 // Workgroups of `count` walks in nv value blocks, `share` walks with common q, k rows:

@@ -6,6 +6,9 @@
 //
 //   S_bar = e^g S;  y = v - S_bar^T k;  u = beta y;  S = S_bar + k u^T;  o = scale S^T q
 // Both reductions over the key channels run in one sweep (o = S_bar^T q + (k.q) u).
+//
+// Bound by reading and writing the states: 240 slots of 96 heads, 128 x 128, two tokens
+// each, 500-545 us, 5.8 TB/s; one token of 32 heads 6.5 us, the chain of one workgroup.
 #include "kda_gdr_device.h"
 #include "kda_launch.h"
 

@@ -20,7 +20,9 @@
 //
 // It is bound by reading: 64 tokens, 64 KB of S and dS, 80 KB of rows.  A workgroup's
 // phases are chained by barriers, so its 80 KB of LDS and 128 registers are held to
-// where two share a CU and one reads while the other computes.
+// where two share a CU and one reads while the other computes.  96 heads of 128, 4096
+// tokens: 310-330 us, 3.4 TB/s (with every operand read into registers by each wave that
+// uses it, one workgroup a CU: 750 us).
 //
 // E1, E2 are kept in two bf16 terms: they enter dG once by rows and once by columns
 // and mostly cancel there, so one rounding each would leave dg with a relative error

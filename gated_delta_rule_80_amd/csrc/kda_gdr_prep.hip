@@ -10,9 +10,11 @@
 // from the blocks below them by T_ij = -T_ii sum_k A_ik T_kj, diagonal by
 // diagonal, in float32 throughout.
 //
-// It is bound by the records it writes (20 KB a chunk beside 32 KB of rows read: 3.6
-// TB/s at 64k tokens, 12 heads); one workgroup for all value heads of a key head,
-// which forms the products once, measured 10% slower at 2 heads a key head.
+// What bounds it: the rows read (32 KB a chunk) and the record written (20 KB), 3.8 TB/s
+// at 64k tokens of 12 heads of 128 (150-170 us), while four workgroups a CU hide the
+// chain of barriers of one (three, at 140 registers a lane, took 180-200 us).  One
+// workgroup for all value heads of a key head, which forms the products once, measured
+// 10% slower at 2 heads a key head.
 #include "kda_gdr_device.h"
 #include "kda_launch.h"
 

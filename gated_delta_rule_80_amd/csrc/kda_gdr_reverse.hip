@@ -11,7 +11,11 @@
 //
 // It reads nothing of the forward walk (S, Y come in with the gradient kernel only), so
 // both run in one launch, the reverse ones first: where the sequences are few or unlike,
-// neither fills the card.
+// neither fills the card.  Measured with bf16, D = 128: 160 us where one after the other
+// took 254 us (packed, 1 to 1500 tokens, 32 heads), 440-480 us against 510 us (96 heads,
+// 4096 tokens: each in halves of a head by itself, together in whole ones).  A reverse
+// chunk of a whole head takes 7 us, 170 products a wave and the splits of four operands
+// (dY, co dO, cx dX, dS); like the forward walk it is bound by issuing them.
 #include "kda_gdr_walk.h"
 
 namespace kda {

@@ -13,7 +13,8 @@ __global__ __launch_bounds__(64 * WV) void kda_gdr_walk_kernel(GdrWalkParams p, 
 // p.starts from s = 1 on.  One workgroup per (walk, 16 value columns): a wave owns 16
 // rows, the start goes round through LDS.  M and the start are split into three bf16
 // terms each (float32 accuracy, 6 products).  Bound by the chain of steps: reading M
-// is kept a step ahead, splitting it spread over as many waves as there are row tiles.
+// is kept a step ahead, splitting it spread over as many waves as there are row tiles
+// (19 steps of 12 heads, D = 128: 48-55 us; with 4 waves and no reads ahead 70 us).
 template <int DK>
 __global__ __launch_bounds__(4 * DK) void kda_gdr_compose_kernel(GdrWalkParams p, int Dv) {
   constexpr int NU = DK / 32, LS = DK + 4;

