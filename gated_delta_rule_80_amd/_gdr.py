@@ -117,7 +117,9 @@ def _rows(t, name, shape, dtype, device):
 def _elsewhere(t):
     """The context that makes t's device current; None if it is."""
     d = t.device
-    if d.type != "cuda" or d.index == torch.cuda.current_device():
+    if d.type != "cuda":
+        raise ValueError(f"libkda works on GPU tensors, not on {d}")
+    if d.index == torch.cuda.current_device():
         return None
     return torch.cuda.device(d)
 

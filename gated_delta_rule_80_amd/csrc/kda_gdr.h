@@ -97,9 +97,17 @@ constexpr bool gdr_whole_head(long walks, int Dv) { return Dv % 128 == 0 && walk
 // walks of 128 chunks: 1280 us as two turns of whole heads, 1090 us so).
 constexpr int gdr_last_walks(long walks) { return walks > 256 && walks % 256 <= 128 ? (int)(walks % 256) : 0; }
 
-// Workgroups of `count` walks in nv value blocks, `share` walks with common q, k rows:
-// whole groups of them, eight at a time (gdr_walk_id).
+// Of `share` walks with common q, k rows, how many stay together: all while there are
+// four groups an XCD, fewer where a group would leave other XCDs idle (64 heads on one key
+// head are a single group).
+constexpr int gdr_walk_group(long count, int share) {
+  while (share > 1 && (count + share - 1) / share < 32) share = (share + 1) / 2;
+  return share;
+}
+// Workgroups of `count` walks in nv value blocks: whole groups, eight at a time
+// (gdr_walk_id).
 constexpr size_t gdr_walk_grid(long count, int share, int nv) {
+  share = gdr_walk_group(count, share);
   return (size_t)((count + share - 1) / share + 7) / 8 * 8 * share * nv;
 }
 

@@ -456,6 +456,7 @@ __device__ __forceinline__ void gdr_copy_flat(char* img, const char* base, int w
 // long sequence's heads and a short one's are spread evenly (packed prompts of 0 to
 // 1024 tokens, 32 heads: 122 us with the walks listed XCD by XCD, 81 us as here).
 __device__ __forceinline__ bool gdr_walk_id(int blk, int nv, int share, int count, int& bh, int& vblk) {
+  share = gdr_walk_group(count, share);
   const int x = blk & 7, i = blk >> 3, unit = share * nv;
   const int member = i % unit;
   bh = (i / unit * 8 + x) * share + member / nv;

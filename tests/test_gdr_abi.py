@@ -377,6 +377,21 @@ def test_binding_type_refusals():
         kda.gdr_decode_args(**dict(d, S=torch.zeros(9, 4, 64, 32)))
 
 
+def test_binding_refuses_host_memory():
+    t = tensors()
+    with pytest.raises(ValueError):
+        kda.kda_gdr_prefill(**t)
+    with pytest.raises(ValueError):
+        kda.kda_gdr_prefill_backward(**t, do=t["v"])
+    with pytest.raises(ValueError):
+        kda.kda_gdr_decode(*(t[n][:, 0].contiguous() for n in ("q", "k", "v", "g", "beta")), t["S0"])
+    p, i = torch.zeros(1, 4, 8), torch.zeros(4, dtype=torch.int32)
+    for call in (lambda: kda.kda_pages_fork(p, i, i), lambda: kda.kda_pages_free(i, i),
+                 lambda: kda.kda_pages_compact(p, i), lambda: kda.kda_pages_copy(p, p, i, i)):
+        with pytest.raises(ValueError):
+            call()
+
+
 def test_binding_pools():
     p = torch.zeros(3, 10, 4, 8)
     a = kda.pages_pool(p)

@@ -130,6 +130,14 @@ def test_many_walks(B, io):
     check_backward(d, opt, io)
 
 
+@pytest.mark.parametrize("io", ["bf16", "fp32"])
+@pytest.mark.parametrize("Hk,Hv", [(1, 40), (3, 9), (1, 7)])
+def test_many_heads_on_one_key_head(Hk, Hv, io):
+    d, opt = make(2, 75, Hk, Hv, 64, 32, io, seed=Hv)
+    check_forward(d, opt, io)
+    check_backward(d, opt, io)
+
+
 LENS = [[0, 1, 0, 70, 64, 3, 0, 129, 32, 0], [5], [0, 0, 0], [1] * 40]
 
 
@@ -144,6 +152,23 @@ def test_prefill_packed(lens, io):
     else:
         _, S = forward(d, opt, cu)
         assert torch.equal(S.cpu(), d["S0"])
+
+
+@pytest.mark.parametrize("io", ["bf16", "fp32"])
+def test_packed_many_sequences(io):
+    lens = [i * 7 % 4 for i in range(2500)]
+    T = sum(lens)
+    d, opt = make(1, T, 1, 2, 32, 32, io, n_seqs=len(lens), seed=1)
+    cu = torch.tensor([0] + list(np.cumsum(lens)), dtype=torch.int32)
+    check_forward(d, opt, io, cu)
+    check_backward(d, opt, io, cu)
+
+
+def test_prefill_no_tokens():
+    d, opt = make(2, 0, 1, 2, 32, 64, "bf16")
+    o, S = forward(d, opt)
+    assert o.shape == (2, 0, 2, 64) and torch.equal(S.cpu(), d["S0"])
+    assert not forward(dict(d, S0=None), opt)[1].any()
 
 
 def test_prefill_tokens_outside_sequences_are_left():
