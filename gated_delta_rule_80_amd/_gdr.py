@@ -71,20 +71,25 @@ def declare(lib):
 
 # ------------------------------------------------------------------ helpers
 # A call on a small model is a few microseconds of GPU time, so the checks below are
-# plain comparisons and only a failing one formats anything.
+# plain comparisons and only a failing one formats anything; devices go by their index
+# (get_device: -1 is the host).
 def _wrong(name, t, shape, dtype, device):
     if t.shape != shape:
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
     if t.dtype != dtype:
         raise TypeError(f"{name} is {t.dtype}, expected {dtype}")
-    raise ValueError(f"{name} is on {t.device}, expected {device}")
+    raise ValueError(f"{name} is on {t.device}, expected {_name(device)}")
+
+
+def _name(device):
+    return "cpu" if device < 0 else f"cuda:{device}"
 
 
 def _dense(t, name, shape, dtype, device):
     """Address of a contiguous tensor of this shape, type and device (None stays None)."""
     if t is None:
         return None
-    if t.shape != shape or t.dtype != dtype or t.device != device:
+    if t.shape != shape or t.dtype is not dtype or t.get_device() != device:
         _wrong(name, t, shape, dtype, device)
     if not t.is_contiguous():
         raise ValueError(f"{name}: libkda needs contiguous tensors")
@@ -93,7 +98,7 @@ def _dense(t, name, shape, dtype, device):
 
 def _rows(t, name, shape, dtype, device):
     """(address, elements between tokens; 0 = packed) of [B, T, H, D] or [N, H, D]."""
-    if t.shape != shape or t.dtype != dtype or t.device != device:
+    if t.shape != shape or t.dtype is not dtype or t.get_device() != device:
         _wrong(name, t, shape, dtype, device)
     if t.is_contiguous():
         return t.data_ptr() or None, 0
@@ -116,16 +121,22 @@ def _rows(t, name, shape, dtype, device):
 
 def _elsewhere(t):
     """The context that makes t's device current; None if it is."""
-    d = t.device
-    if d.type != "cuda":
-        raise ValueError(f"libkda works on GPU tensors, not on {d}")
-    if d.index == torch.cuda.current_device():
+    d = t.get_device()
+    if d < 0:
+        raise ValueError(f"libkda works on GPU tensors, not on {t.device}")
+    if d == torch.cuda.current_device():
         return None
     return torch.cuda.device(d)
 
 
+# the current stream's handle without making a Stream object of it (2 us)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _handle(stream, device):
     if stream is None:
+        if _raw_stream is not None:
+            return _raw_stream(device)
         return torch.cuda.current_stream(device).cuda_stream
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else stream
 
@@ -148,8 +159,8 @@ def _made(stream, device, *tensors):
 def _scratch(need, device, stream, own):
     """(address, bytes) of the workspace, and what keeps it."""
     if own is not None:
-        if own.device != device:
-            raise ValueError(f"workspace is on {own.device}, expected {device}")
+        if own.get_device() != device:
+            raise ValueError(f"workspace is on {own.device}, expected {_name(device)}")
         return (_lib._ptr(own), own.numel() * own.element_size()), own
     if need == 0:
         return (None, 0), None
@@ -167,8 +178,8 @@ def _list(t, name, device):
     """Address of an int32 list on the device."""
     if t.dtype != torch.int32:
         raise TypeError(f"{name} must be int32")
-    if t.device != device:
-        raise ValueError(f"{name} is on {t.device}, expected {device}")
+    if t.get_device() != device:
+        raise ValueError(f"{name} is on {t.device}, expected {_name(device)}")
     return _lib._ptr(t)
 
 
@@ -185,7 +196,7 @@ def gdr_args(q, k, v, g, beta, S0=None, o=None, S_T=None, *, scale=1.0, l2norm_q
     qs, vs = q.shape, v.shape
     B, T, Hk, Dk = qs
     Hv, Dv = vs[2:]
-    io, dev, f32 = q.dtype, q.device, torch.float32
+    io, dev, f32 = q.dtype, q.get_device(), torch.float32
     gates = (B, T, Hv)
     cu, n, NS = None, 0, B
     if cu_seqlens is not None:
@@ -235,7 +246,7 @@ def kda_gdr_prefill(q, k, v, g, beta, S0=None, *, scale=1.0, l2norm_qk=True, eps
             return kda_gdr_prefill(q, k, v, g, beta, S0, scale=scale, l2norm_qk=l2norm_qk, eps=eps, A_log=A_log,
                                    dt_bias=dt_bias, beta_logits=beta_logits, cu_seqlens=cu_seqlens, o=o, S_T=S_T,
                                    workspace=workspace, stream=stream)
-    dev = q.device
+    dev = q.get_device()
     if o is None:
         o = torch.empty(v.shape, dtype=q.dtype, device=dev)
         if stream is not None:
@@ -292,7 +303,7 @@ def kda_gdr_prefill_backward(q, k, v, g, beta, S0=None, *, do, dS_T=None, scale=
             return kda_gdr_prefill_backward(q, k, v, g, beta, S0, do=do, dS_T=dS_T, scale=scale, l2norm_qk=l2norm_qk,
                                             eps=eps, A_log=A_log, dt_bias=dt_bias, beta_logits=beta_logits,
                                             cu_seqlens=cu_seqlens, workspace=workspace, stream=stream)
-    dev, io = q.device, q.dtype
+    dev, io = q.get_device(), q.dtype
     B, T, Hk, Dk = q.shape
     Hv, Dv = v.shape[2:]
     NS = B if cu_seqlens is None else _sequences(cu_seqlens)
@@ -329,7 +340,7 @@ def gdr_decode_args(q, k, v, g, beta, S, slots=None, o=None, *, scale=1.0, l2nor
     qs, vs = q.shape, v.shape
     N, Hk, Dk = qs
     Hv, Dv = vs[1:]
-    io, dev, f32 = q.dtype, q.device, torch.float32
+    io, dev, f32 = q.dtype, q.get_device(), torch.float32
     at = None
     if slots is not None:
         if slots.shape != (N,):
@@ -367,7 +378,7 @@ def kda_gdr_decode(q, k, v, g, beta, S, slots=None, *, scale=1.0, l2norm_qk=True
         with away:
             return kda_gdr_decode(q, k, v, g, beta, S, slots, scale=scale, l2norm_qk=l2norm_qk, eps=eps, A_log=A_log,
                                   dt_bias=dt_bias, beta_logits=beta_logits, o=o, stream=stream)
-    dev = q.device
+    dev = q.get_device()
     if o is None:
         o = (torch.empty if slots is None else torch.zeros)(v.shape, dtype=q.dtype, device=dev)
         if stream is not None:
@@ -409,7 +420,7 @@ def kda_pages_fork(pool, refs, src, *, refs_out=None, dst=None, workspace=None, 
     if away is not None:
         with away:
             return kda_pages_fork(pool, refs, src, refs_out=refs_out, dst=dst, workspace=workspace, stream=stream)
-    dev, i32 = pool.device, torch.int32
+    dev, i32 = pool.get_device(), torch.int32
     p = pages_pool(pool)
     n, pages = src.numel(), (p.n_pages,)
     if refs_out is None:
@@ -436,7 +447,7 @@ def kda_pages_free(refs, pages, *, refs_out=None, stream=None):
     if away is not None:
         with away:
             return kda_pages_free(refs, pages, refs_out=refs_out, stream=stream)
-    dev, i32, shape = refs.device, torch.int32, (refs.numel(),)
+    dev, i32, shape = refs.get_device(), torch.int32, (refs.numel(),)
     if refs_out is None:
         refs_out = torch.empty(shape, dtype=i32, device=dev)
         if stream is not None:
@@ -458,7 +469,7 @@ def kda_pages_compact(pool, refs, table=None, *, refs_out=None, new_id=None, tab
         with away:
             return kda_pages_compact(pool, refs, table, refs_out=refs_out, new_id=new_id, table_out=table_out,
                                      workspace=workspace, stream=stream)
-    dev, i32 = pool.device, torch.int32
+    dev, i32 = pool.get_device(), torch.int32
     p = pages_pool(pool)
     pages = (p.n_pages,)
     if refs_out is None:
@@ -493,8 +504,8 @@ def kda_pages_copy(src_pool, dst_pool, src, dst, *, done=None, workspace=None, s
     if away is not None:
         with away:
             return kda_pages_copy(src_pool, dst_pool, src, dst, done=done, workspace=workspace, stream=stream)
-    dev = dst_pool.device
-    if src_pool.device != dev:
+    dev = dst_pool.get_device()
+    if src_pool.get_device() != dev:
         raise ValueError("both pools must be on one device")
     ps, pd = pages_pool(src_pool), pages_pool(dst_pool)
     n = src.numel()
