@@ -83,7 +83,13 @@ template <int DK, int DV, typename IO> struct GradShape {
   static constexpr int RED = WC * 4 * C * 4 + NW * 4;
   static constexpr int mx(int a, int b) { return a > b ? a : b; }
   // q, k | dO, dX, Y, then the four lists, then the sums over the waves
-  static constexpr int LDS = 2 * ROWK + mx(mx(3 * ROWV, 4 * LIST), RED);
+  static constexpr int BODY = 2 * ROWK + mx(mx(3 * ROWV, 4 * LIST), RED);
+  // the scalars' copy, where two workgroups a CU leave room for it (all shapes but
+  // 128 x 128, where they are read from the record); a phase of a small call would
+  // otherwise begin with a wait for memory
+  static constexpr int SCB = kGdrScalars * C * 4;
+  static constexpr bool SCL = BODY + 2 * SCB <= 81920;
+  static constexpr int LDS = BODY + (SCL ? 2 * SCB : 0);
 };
 
 template <int DK, int DV, typename IO, bool MULTI>
@@ -110,8 +116,11 @@ __global__ __launch_bounds__((GradShape<DK, DV, IO>::NT), 4) void kda_gdr_grad_k
   int lane = tid & 63, r = lane & 15, g4 = lane >> 4;
   // what a phase reads is addressed in that phase: kept from one to the next (or over
   // the heads), the addresses and scalars would fill the registers
-  const float* sc = nullptr;
+  const float* sc = nullptr;  // [scalar][token]: in the record, or
+  const float* scl = nullptr; // the copy in LDS
   int fresh = 0;
+  auto sc1 = [&](int i) { return GS::SCL ? scl[i] : sc[i]; };
+  auto sc4 = [&](int i) { return *reinterpret_cast<const f32x4*>(GS::SCL ? scl + i : sc + i); };
   auto afresh = [&](const float* base) {
     __builtin_amdgcn_sched_barrier(0);
     asm volatile("" : "+v"(lane), "+s"(fresh));
@@ -146,6 +155,11 @@ __global__ __launch_bounds__((GradShape<DK, DV, IO>::NT), 4) void kda_gdr_grad_k
     const size_t rec = ch0.rec + (size_t)gi;  // records of neighbouring heads are neighbours
     const float* const scalars = reinterpret_cast<const float*>(p.rec + rec * R.bytes + R.sc);  // [scalar][token]
     afresh(scalars);
+    if constexpr (GS::SCL) {  // two copies in turn: wave 0 may still read the last head's
+      char* to = lds + GS::BODY + (gi & 1) * GS::SCB;
+      gdr_copy_flat<NT, GS::SCB>(to, reinterpret_cast<const char*>(scalars), wave);
+      scl = reinterpret_cast<const float*>(to);
+    }
     const size_t vo = ch0.tok * HD + (size_t)h * DV;
     GdrCopy<NT, C, DV, IO>::part(area, static_cast<const IO*>(p.dO) + vo, HD, n - 1, wave);
     GdrCopy<NT, C, DV, IO>::part(area + GS::ROWV, static_cast<const IO*>(p.dv) + vo, HD, n - 1, wave);
@@ -178,7 +192,7 @@ __global__ __launch_bounds__((GradShape<DK, DV, IO>::NT), 4) void kda_gdr_grad_k
           gmma(aq, fS[u], g_row<IO, DV>(iO, tk, u, g4));
           gmma(ae, fS[u], g_row<IO, DV>(iX, tk, u, g4));
         }
-        const float gam = exp2_fast(sc[5 * C + tk] + sc[6 * C + tk]);
+        const float gam = exp2_fast(sc1(5 * C + tk) + sc1(6 * C + tk));
         qd[t] = ke[t] = 0.f;
         if (MULTI) {  // this head's dots: those of the sums, less what the heads before left
           const f32x4 k4 = g_four<IO, DK>(iK, tk, c0 + 4 * g4), q4 = g_four<IO, DK>(iQ, tk, c0 + 4 * g4);
@@ -214,7 +228,7 @@ __global__ __launch_bounds__((GradShape<DK, DV, IO>::NT), 4) void kda_gdr_grad_k
 #pragma unroll
         for (int u = 0; u < NUV; ++u) gmma(aw[t], fD[u], g_row<IO, DV>(iY, tk, u, g4));
         const float lam =
-            exp2_fast((sc[5 * C + C - 1] - sc[5 * C + tk]) + (sc[6 * C + C - 1] - sc[6 * C + tk]));
+            exp2_fast((sc1(5 * C + C - 1) - sc1(5 * C + tk)) + (sc1(6 * C + C - 1) - sc1(6 * C + tk)));
         const f32x4 k4 = g_four<IO, DK>(iK, tk, c0 + 4 * g4);
         kw1[t] = 0.f;
 #pragma unroll
@@ -256,17 +270,17 @@ __global__ __launch_bounds__((GradShape<DK, DV, IO>::NT), 4) void kda_gdr_grad_k
         for (int s = 0; s < TPU; ++s) gmma(m[s], g_row<IO, DV>(ra, Op::perm(TPU * u + s, r), v, g4), fb);
         if (v % 2 == 1) __builtin_amdgcn_sched_barrier(0);
       }
-      const float Gh = sc[5 * C + tk], Gl = sc[6 * C + tk];
+      const float Gh = sc1(5 * C + tk), Gl = sc1(6 * C + tk);
       const float sign = by_row ? 1.f : -1.f, sg = second ? -1.f : by_row ? 1.f : p.scale;
       const int dir = by_row ? 1 : -1, least = second ? 1 : 0;
-      const float* f0 = sc + (by_row || second ? 3 : 4) * C;
+      const int f0 = (by_row || second ? 3 : 4) * C;
 #pragma unroll
       for (int s = 0; s < TPU; ++s) {
         const int x4 = Op::row4(TPU * u + s, g4);
-        const f32x4 hx = *reinterpret_cast<const f32x4*>(sc + 5 * C + x4),
-                    lx = *reinterpret_cast<const f32x4*>(sc + 6 * C + x4);
-        f32x4 fx = *reinterpret_cast<const f32x4*>(f0 + x4);
-        if (by_row) fx *= *reinterpret_cast<const f32x4*>(sc + 7 * C + x4);
+        const f32x4 hx = sc4(5 * C + x4),
+                    lx = sc4(6 * C + x4);
+        f32x4 fx = sc4(f0 + x4);
+        if (by_row) fx *= sc4(7 * C + x4);
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           const float d = exp2_fast(sign * ((Gh - hx[e]) + (Gl - lx[e]))) * (fx[e] * sg);
@@ -323,7 +337,7 @@ __global__ __launch_bounds__((GradShape<DK, DV, IO>::NT), 4) void kda_gdr_grad_k
 #pragma unroll
     for (int t = 0; t < TW; ++t) {
       const int tk = Op::perm(t0 + t, r);
-      const float bt = sc[7 * C + tk];
+      const float bt = sc1(7 * C + tk);
       const f32x4 k4 = g_four<IO, DK>(iK, tk, c0 + 4 * g4), q4 = g_four<IO, DK>(iQ, tk, c0 + 4 * g4);
       kw[t] = 0.f;
 #pragma unroll
@@ -362,13 +376,13 @@ __global__ __launch_bounds__((GradShape<DK, DV, IO>::NT), 4) void kda_gdr_grad_k
     if (MULTI) __syncthreads();  // the sums have been read
     if (wave == 0) {
       const int at_sc = lane < C ? lane : C - 1;
-      const float bt = sc[7 * C + at_sc], rk = sc[3 * C + at_sc], rq = sc[4 * C + at_sc];
+      const float bt = sc1(7 * C + at_sc), rk = sc1(3 * C + at_sc), rq = sc1(4 * C + at_sc);
       totq += q;
       totk += fmaf(bt, w, e);
       w *= rk;
       float dG = fmaf(q, rq * p.scale, e * rk) - bt * w;
       k1 = group_sum<64>(k1 * rk * bt);
-      if (lane == C - 1) dG += exp2_fast(sc[5 * C + C - 1] + sc[6 * C + C - 1]) * all + k1;
+      if (lane == C - 1) dG += exp2_fast(sc1(5 * C + C - 1) + sc1(6 * C + C - 1)) * all + k1;
 #pragma unroll
       for (int m = 1; m < C; m <<= 1) {
         const float y = __shfl_down(dG, m, 64);
@@ -389,10 +403,11 @@ __global__ __launch_bounds__((GradShape<DK, DV, IO>::NT), 4) void kda_gdr_grad_k
     }
   }
   // ---- through the norms, to the raw rows: x / |x|, dx = (dy - x^ (x^ . dy)) / |x|
-  sc = reinterpret_cast<const float*>(p.rec + ch0.rec * R.bytes + R.sc);
+  // (the norms of q and k, the same in every head's record)
+  if (!GS::SCL) sc = reinterpret_cast<const float*>(p.rec + ch0.rec * R.bytes + R.sc);
   __syncthreads();
   if (wave == 0 && lane < C) {
-    const float rq = sc[4 * C + lane], rk = sc[3 * C + lane];
+    const float rq = sc1(4 * C + lane), rk = sc1(3 * C + lane);
     red[lane] = p.l2 ? totq * rq * rq : 0.f;
     red[C + lane] = p.l2 ? totk * rk * rk : 0.f;
   }
@@ -400,7 +415,7 @@ __global__ __launch_bounds__((GradShape<DK, DV, IO>::NT), 4) void kda_gdr_grad_k
 #pragma unroll
   for (int t = 0; t < TW; ++t) {  // over the lane's own elements of q and k
     const int tk = Op::perm(t0 + t, r);
-    const float rq = p.scale * sc[4 * C + tk], rk = sc[3 * C + tk], qd = red[tk], kd = red[C + tk];
+    const float rq = p.scale * sc1(4 * C + tk), rk = sc1(3 * C + tk), qd = red[tk], kd = red[C + tk];
     const f32x4 k4 = g_four<IO, DK>(iK, tk, c0 + 4 * g4), q4 = g_four<IO, DK>(iQ, tk, c0 + 4 * g4);
     float dq[4], dk[4];
 #pragma unroll
