@@ -143,7 +143,7 @@ struct GdrWalkParams {
   // (the first from S0) for its N and with V = 0 from I for its M, then the starts
   // are composed in order, then every segment is walked with its output.
   //   starts [B Hv][nseg][Dk][Dv] float32: at index s + 1 first the N of segment s,
-  //          then the state at the start of segment s + 1 (index 0: not used)
+  //          then the state at the start of segment s + 1; index 0: S0
   //   maps   [B Hv][nseg][Dk][Dk] float32: M of segments 1 .. nseg - 2
   int nseg, seg_len;
   float* starts;

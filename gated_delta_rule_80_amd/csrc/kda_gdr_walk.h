@@ -127,7 +127,7 @@ __device__ __forceinline__ void gdr_walk(const GdrWalkParams& p, int Dv, int blk
   const float* s_in = p.S0 != nullptr && seg == 0 ? p.S0 + sbase : nullptr;
   float* s_out = p.S_T != nullptr ? p.S_T + sbase : nullptr;
   if (p.nseg > 1) {
-    if (p.pass == 0 && seg > 0) s_in = p.starts + seg_at;
+    if (p.pass == 0) s_in = p.starts + seg_at;
     if (p.pass == 0 && seg < p.nseg - 1) s_out = nullptr;
     if (p.pass == 1) s_out = p.starts + seg_at + (size_t)DK * Dv;
     if (p.pass == 2) s_out = p.maps + seg_at;
@@ -145,6 +145,16 @@ __device__ __forceinline__ void gdr_walk(const GdrWalkParams& p, int Dv, int blk
       for (int t = 0; t < CT; ++t)
 #pragma unroll
         for (int e = 0; e < 4; ++e) S[v][t][e] = s_in[16 * v + (size_t)(Op::row4(t, g4) + e) * Dv];
+  }
+  if (p.nseg > 1 && p.pass == 1 && seg == 0) {
+    // kept for the pass with outputs, whose last segments may write S_T over S0
+#pragma unroll
+    for (int v = 0; v < NV; ++v)
+#pragma unroll
+      for (int t = 0; t < CT; ++t)
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          p.starts[seg_at + 16 * v + (size_t)(Op::row4(t, g4) + e) * Dv] = S[v][t][e];
   }
 #pragma unroll
   for (int v = 0; v < NV; ++v)

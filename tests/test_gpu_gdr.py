@@ -117,8 +117,11 @@ def test_prefill_split(shape, rate, io):
     """Few long rows, whose walks are cut into segments; the state carries far, so
     the segments' maps count."""
     d, opt = make(*shape, io, seed=shape[1], rate=rate)
-    check_forward(d, opt, io)
+    o, S = check_forward(d, opt, io)
     check_forward(dict(d, S0=None), opt, io)
+    x = d["S0"].cuda()  # the state in place
+    o2, _ = kda.kda_gdr_prefill(*[d[n].cuda() for n in ("q", "k", "v", "g", "beta")], x, S_T=x)
+    assert torch.equal(o, o2) and torch.equal(S, x)
 
 
 @pytest.mark.parametrize("io", ["bf16", "fp32"])
