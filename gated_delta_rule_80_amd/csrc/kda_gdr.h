@@ -149,6 +149,7 @@ struct GdrWalkParams {
   float* starts;
   float* maps;
   int pass;  // 0: outputs; 1: N; 2: M
+  int bwd;   // the records are the backward's
   int walk0, walks;  // set by the launcher: a launch's share of the walks (or segments)
 };
 
@@ -162,6 +163,15 @@ struct GdrReverseParams {
   float* dS0;         // NULL: not written
   void* dv;           // [B][T][Hv][Dv]
   void* ckpt;         // the gradient of each chunk's end state, layout as above
+  // split as the forward walk: dS is affine too, dS_start = M^T dS_end + N' with the M of
+  // the state, so every segment but the first is walked for its N' (pass 1, dS_end = 0;
+  // the last from dS_T), the ends are composed from the last to the first, and every
+  // segment is walked with its outputs (pass 0).
+  //   ends [B Hv][nseg][Dk][Dv] float32: at index s - 1 first the N' of segment s, then
+  //        the gradient at the end of segment s - 1 (the last index: not used)
+  int nseg, seg_len;
+  float* ends;
+  int pass, walks;    // set by the launcher
 };
 
 struct GdrGradParams {

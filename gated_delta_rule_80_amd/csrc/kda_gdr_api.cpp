@@ -130,10 +130,11 @@ kda_status disjoint(const Spans& outs, const Spans& ins) {
   return KDA_OK;
 }
 
-// The workspace: sequence tables, the chunk records, and for the backward Y, the
-// two checkpoints per chunk and the float32 gradient of the decay.
+// The workspace: sequence tables, the chunk records, for the backward Y, the two
+// checkpoints per chunk and the float32 gradient of the decay, and of a split walk the
+// segments' starts, maps and (backward) ends.
 struct GdrWork {
-  size_t seq, rec, y, ckS, ckdS, dg, starts, maps, bytes;
+  size_t seq, rec, y, ckS, ckdS, dg, starts, maps, ends, bytes;
 };
 GdrSplit split_of(const kda_gdr_args* a, const GdrSizes& s) {
   if (gdr_packed(a) || a->T == 0) return {1, s.NT};
@@ -156,13 +157,14 @@ bool gdr_work(const kda_gdr_args* a, const GdrSizes& s, bool bwd, GdrWork& w) {
   w.ckS = round_up(w.y + y, 256);
   w.ckdS = round_up(w.ckS + ck, 256);
   w.dg = round_up(w.ckdS + ck, 256);
-  w.starts = w.maps = round_up(w.dg + dg, 256);
+  w.starts = w.maps = w.ends = round_up(w.dg + dg, 256);
   w.bytes = w.starts;
-  if (const GdrSplit sp = split_of(a, s); !bwd && sp.nseg > 1) {
+  if (const GdrSplit sp = split_of(a, s); sp.nseg > 1) {
     // at most 256 workgroups of segments: these sizes stay small
     const size_t n = (size_t)a->B * a->Hv * sp.nseg * a->Dk * 4;
     w.maps = w.starts + n * a->Dv;
-    w.bytes = w.maps + n * a->Dk;
+    w.ends = w.maps + n * a->Dk;
+    w.bytes = w.ends + (bwd ? n * a->Dv : 0);
   }
   return w.bytes < (size_t(1) << 62);
 }
@@ -344,6 +346,12 @@ kda_status kda_gdr_prefill_backward(const kda_gdr_backward_args* a, void* ws, si
   p.S0 = f->S0;
   p.y = base + w.y;
   p.ckpt = base + w.ckS;
+  p.bwd = 1;
+  const GdrSplit sp = split_of(f, s);
+  p.nseg = sp.nseg;
+  p.seg_len = sp.seg_len;
+  p.starts = reinterpret_cast<float*>(base + w.starts);
+  p.maps = reinterpret_cast<float*>(base + w.maps);
   GdrReverseParams rv{};
   rv.s = g;
   rv.q = f->q; rv.k = f->k;
@@ -351,6 +359,9 @@ kda_status kda_gdr_prefill_backward(const kda_gdr_backward_args* a, void* ws, si
   rv.dO = a->dO; rv.dS_T = a->dS_T; rv.dS0 = a->dS0;
   rv.dv = a->dv;
   rv.ckpt = base + w.ckdS;
+  rv.nseg = sp.nseg;
+  rv.seg_len = sp.seg_len;
+  rv.ends = reinterpret_cast<float*>(base + w.ends);
   if (kda_status e = hip_status(launch_gdr_two_walks(rv, p, f->Dk, f->Dv, fp32, st)); e != KDA_OK) return e;
   GdrGradParams d{};
   d.s = g;

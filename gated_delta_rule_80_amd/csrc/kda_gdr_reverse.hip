@@ -35,7 +35,8 @@ struct GdrReverseLds {
   static constexpr int BYTES = DO + C * VB * ES;
 };
 
-template <int DK, int WV, int NV, typename IO>
+// STORE: with the outputs (dv, the kept dS)
+template <int DK, int WV, int NV, typename IO, bool STORE>
 __device__ __forceinline__ void gdr_reverse(const GdrReverseParams& p, int Dv, int blk, char* lds) {
   using L = GdrReverseLds<DK, WV, NV, IO>;
   using Op = GOp<IO>;
@@ -46,12 +47,24 @@ __device__ __forceinline__ void gdr_reverse(const GdrReverseParams& p, int Dv, i
   constexpr int NUK = DK / Op::KU, NUC = C / Op::KU;
   constexpr int TPU = Op::TPU, TT = L::TT, ES = L::ES;
   constexpr GdrRecord R = gdr_record(F32, true);
-  constexpr int NSTORE = NV * (F32 ? 4 : 1) * (CT + TL);  // stores of a chunk
+  constexpr int NSTORE = STORE ? NV * (F32 ? 4 : 1) * (CT + TL) : 0;  // stores of a chunk
   const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6), r = lane & 15, g4 = lane >> 4;
-  int bh, vblk;
-  if (!gdr_walk_id(blk, Dv / VB, p.s.Hv / p.s.Hk, p.s.NS * p.s.Hv, bh, vblk)) return;  // uniform
+  int bh, vblk, seg = 0;
+  if (!gdr_walk_id(blk, Dv / VB, p.s.Hv / p.s.Hk, p.walks, bh, vblk)) return;  // uniform
+  if (p.nseg > 1) {
+    const int walks = p.s.B * p.s.Hv;
+    seg = bh / walks + p.pass;  // the first segment needs no N'
+    bh %= walks;
+  }
   const int h = bh % p.s.Hv, b = bh / p.s.Hv, hk = h / (p.s.Hv / p.s.Hk);
-  const GdrSpan sp = gdr_span(p.s, b, h, C);
+  GdrSpan sp = gdr_span(p.s, b, h, C);
+  if (p.nseg > 1) {
+    const int c0 = seg * p.seg_len;
+    sp.tok0 += (long)c0 * C;
+    sp.Tq -= c0 * C;
+    sp.nch = sp.nch - c0 < p.seg_len ? sp.nch - c0 : p.seg_len;
+    sp.rec0 += c0 * sp.rstride;
+  }
   const int v0 = vblk * VB + 16 * NV * wave;  // this wave's value columns
   const long HD = (long)p.s.Hv * Dv;
 
@@ -97,13 +110,22 @@ __device__ __forceinline__ void gdr_reverse(const GdrReverseParams& p, int Dv, i
   for (int v = 0; v < NV; ++v)
 #pragma unroll
     for (int t = 0; t < CT; ++t) dS[v][t] = f32x4{0.f, 0.f, 0.f, 0.f};
-  if (p.dS_T != nullptr) {
+  // where this walk's gradient comes from (NULL: zeros) and goes to (NULL: nowhere)
+  const float* d_in = p.dS_T != nullptr ? p.dS_T + sbase : nullptr;
+  float* d_out = p.dS0 != nullptr ? p.dS0 + sbase : nullptr;
+  if (p.nseg > 1) {
+    float* ends = p.ends + ((size_t)bh * p.nseg + seg) * DK * Dv + v0 + r;
+    if (seg < p.nseg - 1) d_in = STORE ? ends : nullptr;
+    if (!STORE) d_out = ends - (size_t)DK * Dv;
+    else if (seg > 0) d_out = nullptr;
+  }
+  if (d_in != nullptr) {
 #pragma unroll
     for (int v = 0; v < NV; ++v)
 #pragma unroll
       for (int t = 0; t < CT; ++t)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) dS[v][t][e] = p.dS_T[sbase + 16 * v + (size_t)(Op::row4(t, g4) + e) * Dv];
+        for (int e = 0; e < 4; ++e) dS[v][t][e] = d_in[16 * v + (size_t)(Op::row4(t, g4) + e) * Dv];
   }
 #pragma unroll
   for (int v = 0; v < NV; ++v)
@@ -268,7 +290,7 @@ __device__ __forceinline__ void gdr_reverse(const GdrReverseParams& p, int Dv, i
     __builtin_amdgcn_sched_barrier(0);
     if (n > 0) copy(n - 1, nbuf, 2);
     __builtin_amdgcn_sched_barrier(0);  // the stores counted above come after the copies
-    {
+    if constexpr (STORE) {
       const BufRes to = make_buf(static_cast<IO*>(p.ckpt) + (sp.rec0 + n * sp.rstride) * (size_t)DK * Dv,
                                  (unsigned)(DK * Dv * ES));
 #pragma unroll
@@ -309,7 +331,7 @@ __device__ __forceinline__ void gdr_reverse(const GdrReverseParams& p, int Dv, i
     // ---- slot 6: dS -= K^T (cx dX), second half, beside the split of the first
     add_t(iK, x3, 1);
     x_of(0);
-    {
+    if constexpr (STORE) {
       // rows behind the sequence's end lie behind the buffer
       const int left = sp.Tq - n * C < C ? sp.Tq - n * C : C;
       const BufRes to = make_buf(static_cast<IO*>(p.dv) + (size_t)(sp.tok0 + n * C) * HD,
@@ -328,13 +350,13 @@ __device__ __forceinline__ void gdr_reverse(const GdrReverseParams& p, int Dv, i
 #pragma unroll
       for (int u = 0; u < NUK; ++u) s2[v][u].set(&dS[v][TPU * u]);
   }
-  if (p.dS0 != nullptr) {
+  if (d_out != nullptr) {
 #pragma unroll
     for (int v = 0; v < NV; ++v)
 #pragma unroll
       for (int t = 0; t < CT; ++t)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) p.dS0[sbase + 16 * v + (size_t)(Op::row4(t, g4) + e) * Dv] = dS[v][t][e];
+        for (int e = 0; e < 4; ++e) d_out[16 * v + (size_t)(Op::row4(t, g4) + e) * Dv] = dS[v][t][e];
   }
 }
 
@@ -344,9 +366,22 @@ __global__ __launch_bounds__(64 * WV) void kda_gdr_two_walks_kernel(GdrReversePa
   constexpr int A = GdrReverseLds<DK, WV, NV, IO>::BYTES, B = GdrWalkLds<DK, WV, NV, IO, false>::BYTES;
   __shared__ __attribute__((aligned(16))) char lds[2 * (A > B ? A : B)];
   if ((int)blockIdx.x < half)
-    gdr_reverse<DK, WV, NV, IO>(r, Dv, blockIdx.x, lds);
+    gdr_reverse<DK, WV, NV, IO, true>(r, Dv, blockIdx.x, lds);
   else
     gdr_walk<DK, WV, NV, IO, false, true>(w, Dv, blockIdx.x - half, lds);
+}
+
+template <int DK, int WV, int NV, typename IO>
+__global__ __launch_bounds__(64 * WV) void kda_gdr_reverse_kernel(GdrReverseParams r, int Dv) {
+  __shared__ __attribute__((aligned(16))) char lds[2 * GdrReverseLds<DK, WV, NV, IO>::BYTES];
+  gdr_reverse<DK, WV, NV, IO, false>(r, Dv, blockIdx.x, lds);
+}
+
+template <int DK, int WV, int NV, typename IO>
+static hipError_t launch_ends_t(const GdrReverseParams& r, int Dv, hipStream_t st) {
+  const size_t grid = gdr_walk_grid(r.walks, r.s.Hv / r.s.Hk, Dv / (16 * NV * WV));
+  hipLaunchKernelGGL((kda_gdr_reverse_kernel<DK, WV, NV, IO>), dim3((unsigned)grid), dim3(64 * WV), 0, st, r, Dv);
+  return hipGetLastError();
 }
 
 template <int DK, int WV, int NV, typename IO>
@@ -359,11 +394,25 @@ static hipError_t launch_two_t(const GdrReverseParams& r, const GdrWalkParams& w
 }
 
 template <int DK, typename IO>
-static hipError_t launch_two_w(const GdrReverseParams& r, const GdrWalkParams& all, int Dv, hipStream_t st) {
-  GdrWalkParams w = all;
-  w.nseg = 1;
-  w.pass = w.walk0 = 0;
-  w.walks = r.s.NS * r.s.Hv;
+static hipError_t launch_two_w(const GdrReverseParams& all_r, const GdrWalkParams& all_w, int Dv, hipStream_t st) {
+  GdrReverseParams r = all_r;
+  GdrWalkParams w = all_w;
+  const int rows = r.s.NS * r.s.Hv;
+  if (w.nseg > 1) {
+    if (hipError_t e = launch_gdr_maps(w, DK, Dv, sizeof(IO) == 4, st); e != hipSuccess) return e;
+    r.pass = 1;
+    r.walks = rows * (r.nseg - 1);
+    hipError_t e;
+    if (Dv == 32) e = launch_ends_t<DK, 2, 1, IO>(r, Dv, st);
+    else if (sizeof(IO) == 2 && gdr_whole_head(r.walks, Dv)) e = launch_ends_t<DK, sizeof(IO) == 2 ? 8 : 4, 1, IO>(r, Dv, st);
+    else e = launch_ends_t<DK, 4, 1, IO>(r, Dv, st);
+    if (e != hipSuccess) return e;
+    GdrWalkParams c = w;
+    c.starts = r.ends;
+    if (e = launch_gdr_compose(c, DK, Dv, true, st); e != hipSuccess) return e;
+  }
+  w.pass = w.walk0 = r.pass = 0;
+  w.walks = r.walks = rows * (w.nseg > 1 ? w.nseg : 1);
   if (Dv == 32) return launch_two_t<DK, 2, 1, IO>(r, w, Dv, st);
   if constexpr (sizeof(IO) == 2)
     if (gdr_whole_head(2l * w.walks, Dv)) return launch_two_t<DK, 8, 1, IO>(r, w, Dv, st);

@@ -57,6 +57,10 @@ __device__ __forceinline__ void gdr_walk(const GdrWalkParams& p, int Dv, int blk
   // stores of a chunk: o, 4 columns each; or the state and Y
   constexpr int NSTORE = NV * (OUT ? TL : (CK ? (F32 ? 4 : 1) * (CT + TL) : 0));
   static_assert(!(OUT && CK), "the stores are counted for one or the other");
+  // the maps' passes read Tm and the scalars only, which stand alike in both records
+  constexpr GdrRecord RB = gdr_record(F32, true);
+  static_assert(RB.t == R.t && RB.sc == R.sc, "one place in both records");
+  const size_t rec_bytes = !OUT && !CK && p.bwd ? RB.bytes : R.bytes;
   const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6), r = lane & 15, g4 = lane >> 4;
   int bh, vblk, seg = 0;
   if (!gdr_walk_id(blk, Dv / VB, p.s.Hv / p.s.Hk, p.walks, bh, vblk)) return;  // uniform
@@ -94,7 +98,7 @@ __device__ __forceinline__ void gdr_walk(const GdrWalkParams& p, int Dv, int blk
   auto copy = [&](int n, char* buf, int part) {
     const int last = sp.Tq - n * C - 1;  // >= 0: the chunk exists
     const long t0 = (long)n * C;
-    const char* rec = p.rec + (sp.rec0 + n * sp.rstride) * R.bytes;
+    const char* rec = p.rec + (sp.rec0 + n * sp.rstride) * rec_bytes;
     if (part == 0) {
       const IO* pk = kb + t0 * p.s.ks;
       const IO* pv = vb + t0 * p.s.vs;

@@ -10,12 +10,13 @@ __global__ __launch_bounds__(64 * WV) void kda_gdr_walk_kernel(GdrWalkParams p, 
 }
 
 // Composes the segments' starts: start_{s+1} = M_s start_s + N_s, in place in
-// p.starts from s = 1 on.  One workgroup per (walk, 16 value columns): a wave owns 16
+// p.starts from s = 1 on; REV: the gradients at their ends, end_{s-1} = M_s^T end_s +
+// N'_s, from the last segment but one down.  One workgroup per (walk, 16 value columns): a wave owns 16
 // rows, the start goes round through LDS.  M and the start are split into three bf16
 // terms each (float32 accuracy, 6 products).  Bound by the chain of steps: reading M
 // is kept a step ahead, splitting it spread over as many waves as there are row tiles
 // (19 steps of 12 heads, D = 128: 48-55 us; with 4 waves and no reads ahead 70 us).
-template <int DK>
+template <int DK, bool REV>
 __global__ __launch_bounds__(4 * DK) void kda_gdr_compose_kernel(GdrWalkParams p, int Dv) {
   constexpr int NU = DK / 32, LS = DK + 4;
   __shared__ __attribute__((aligned(16))) float st[2][16 * LS];
@@ -36,14 +37,24 @@ __global__ __launch_bounds__(4 * DK) void kda_gdr_compose_kernel(GdrWalkParams p
     float m[NU][8];
     f32x4 n;
   };
-  auto fetch = [&](int s, Rows& x) {
-    s = s < p.nseg - 1 ? s : p.nseg - 2;
+  constexpr int D = REV ? -1 : 1;
+  const int first = REV ? p.nseg - 2 : 1;
+  auto fetch = [&](int i, Rows& x) {  // of step i (past the last: of the last)
+    const int s = first + D * (i < p.nseg - 2 ? i : p.nseg - 3);
 #pragma unroll
-    for (int u = 0; u < NU; ++u) load8(maps + ((size_t)s * DK + row0 + r) * DK + 32 * u + 8 * g4, x.m[u]);
+    for (int u = 0; u < NU; ++u) {
+      if constexpr (REV) {
 #pragma unroll
-    for (int e = 0; e < 4; ++e) x.n[e] = starts[((size_t)(s + 1) * DK + row0 + 4 * g4 + e) * Dv + r];
+        for (int e = 0; e < 8; ++e) x.m[u][e] = maps[((size_t)s * DK + 32 * u + 8 * g4 + e) * DK + row0 + r];
+      } else {
+        load8(maps + ((size_t)s * DK + row0 + r) * DK + 32 * u + 8 * g4, x.m[u]);
+      }
+    }
+#pragma unroll
+    for (int e = 0; e < 4; ++e) x.n[e] = starts[((size_t)(s + D) * DK + row0 + 4 * g4 + e) * Dv + r];
   };
-  auto step = [&](int s, const Rows& x) {
+  auto step = [&](int i, const Rows& x) {
+    const int s = first + D * i;
     const float* in = st[s & 1];
     f32x4 acc = x.n;
 #pragma unroll
@@ -60,21 +71,22 @@ __global__ __launch_bounds__(4 * DK) void kda_gdr_compose_kernel(GdrWalkParams p
     }
     *reinterpret_cast<f32x4*>(&st[(s + 1) & 1][r * LS + row0 + 4 * g4]) = acc;
 #pragma unroll
-    for (int e = 0; e < 4; ++e) starts[((size_t)(s + 1) * DK + row0 + 4 * g4 + e) * Dv + r] = acc[e];
+    for (int e = 0; e < 4; ++e) starts[((size_t)(s + D) * DK + row0 + 4 * g4 + e) * Dv + r] = acc[e];
   };
-  // the start of segment 1, column by column
+  // the state the chain begins with, column by column
   for (int i = tid; i < 16 * DK; i += 4 * DK)
-    st[1][(i & 15) * LS + (i >> 4)] = starts[((size_t)DK + (i >> 4)) * Dv + (i & 15)];
+    st[first & 1][(i & 15) * LS + (i >> 4)] = starts[((size_t)first * DK + (i >> 4)) * Dv + (i & 15)];
+  const int steps = p.nseg - 2;
   Rows x, y;  // of this step and the next, whose reads are under way meanwhile
-  if (p.nseg > 2) fetch(1, x);
+  if (steps > 0) fetch(0, x);
   lds_barrier();
-  for (int s = 1; s < p.nseg - 1; s += 2) {
-    fetch(s + 1, y);
-    step(s, x);
+  for (int i = 0; i < steps; i += 2) {
+    fetch(i + 1, y);
+    step(i, x);
     lds_barrier();
-    if (s + 1 == p.nseg - 1) break;  // uniform
-    fetch(s + 2, x);
-    step(s + 1, y);
+    if (i + 1 == steps) break;  // uniform
+    fetch(i + 2, x);
+    step(i + 1, y);
     lds_barrier();
   }
 }
@@ -119,25 +131,38 @@ static hipError_t launch_walk(const GdrWalkParams& p, int Dk, int Dv, hipStream_
   return hipErrorInvalidValue;
 }
 
-hipError_t launch_gdr_walk(const GdrWalkParams& p, int Dk, int Dv, bool fp32, hipStream_t st) {
-  auto walk = [&](const GdrWalkParams& q, int cols) {
-    return fp32 ? launch_walk<float>(q, Dk, cols, st) : launch_walk<__bf16>(q, Dk, cols, st);
-  };
-  if (p.nseg > 1) {
-    GdrWalkParams q = p;
-    q.pass = 1;
-    if (hipError_t e = walk(q, Dv); e != hipSuccess) return e;
-    q.pass = 2;
-    if (hipError_t e = walk(q, Dk); e != hipSuccess) return e;
-    const dim3 grid((unsigned)((size_t)p.s.B * p.s.Hv * (Dv / 16)));
-    switch (Dk) {
-      case 32: hipLaunchKernelGGL(kda_gdr_compose_kernel<32>, grid, dim3(128), 0, st, p, Dv); break;
-      case 64: hipLaunchKernelGGL(kda_gdr_compose_kernel<64>, grid, dim3(256), 0, st, p, Dv); break;
-      default: hipLaunchKernelGGL(kda_gdr_compose_kernel<128>, grid, dim3(512), 0, st, p, Dv); break;
-    }
-    if (hipError_t e = hipGetLastError(); e != hipSuccess) return e;
+static hipError_t walk(const GdrWalkParams& p, int Dk, int cols, bool fp32, hipStream_t st) {
+  return fp32 ? launch_walk<float>(p, Dk, cols, st) : launch_walk<__bf16>(p, Dk, cols, st);
+}
+
+template <bool REV> static hipError_t launch_compose(const GdrWalkParams& p, int Dk, int Dv, hipStream_t st) {
+  const dim3 grid((unsigned)((size_t)p.s.B * p.s.Hv * (Dv / 16)));
+  switch (Dk) {
+    case 32: hipLaunchKernelGGL((kda_gdr_compose_kernel<32, REV>), grid, dim3(128), 0, st, p, Dv); break;
+    case 64: hipLaunchKernelGGL((kda_gdr_compose_kernel<64, REV>), grid, dim3(256), 0, st, p, Dv); break;
+    case 128: hipLaunchKernelGGL((kda_gdr_compose_kernel<128, REV>), grid, dim3(512), 0, st, p, Dv); break;
+    default: return hipErrorInvalidValue;
   }
-  return walk(p, Dv);
+  return hipGetLastError();
+}
+hipError_t launch_gdr_compose(const GdrWalkParams& p, int Dk, int Dv, bool reverse, hipStream_t st) {
+  return reverse ? launch_compose<true>(p, Dk, Dv, st) : launch_compose<false>(p, Dk, Dv, st);
+}
+
+// the segments' maps, and their starts from them
+hipError_t launch_gdr_maps(const GdrWalkParams& p, int Dk, int Dv, bool fp32, hipStream_t st) {
+  GdrWalkParams q = p;
+  q.pass = 1;
+  if (hipError_t e = walk(q, Dk, Dv, fp32, st); e != hipSuccess) return e;
+  q.pass = 2;
+  if (hipError_t e = walk(q, Dk, Dk, fp32, st); e != hipSuccess) return e;
+  return launch_gdr_compose(p, Dk, Dv, false, st);
+}
+
+hipError_t launch_gdr_walk(const GdrWalkParams& p, int Dk, int Dv, bool fp32, hipStream_t st) {
+  if (p.nseg > 1)
+    if (hipError_t e = launch_gdr_maps(p, Dk, Dv, fp32, st); e != hipSuccess) return e;
+  return walk(p, Dk, Dv, fp32, st);
 }
 
 }  // namespace kda

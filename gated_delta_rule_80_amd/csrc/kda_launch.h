@@ -44,6 +44,8 @@ hipError_t launch_decode(const DecodeParams& p, int D, bool fp32, hipStream_t st
 // the gated delta rule with one decay per head (kda_gdr.h)
 hipError_t launch_gdr_prep(const GdrPrepParams& p, int Dk, bool fp32, bool bwd, hipStream_t st);
 hipError_t launch_gdr_walk(const GdrWalkParams& p, int Dk, int Dv, bool fp32, hipStream_t st);
+hipError_t launch_gdr_maps(const GdrWalkParams& p, int Dk, int Dv, bool fp32, hipStream_t st);
+hipError_t launch_gdr_compose(const GdrWalkParams& p, int Dk, int Dv, bool reverse, hipStream_t st);
 hipError_t launch_gdr_two_walks(const GdrReverseParams& r, const GdrWalkParams& w, int Dk, int Dv, bool fp32,
                                 hipStream_t st);
 hipError_t launch_gdr_grad(const GdrGradParams& p, int Dk, int Dv, bool fp32, hipStream_t st);

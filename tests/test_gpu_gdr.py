@@ -282,6 +282,17 @@ def test_backward_packed(lens, io):
     check_backward(d, opt, io, torch.tensor([0] + list(np.cumsum(lens)), dtype=torch.int32))
 
 
+@pytest.mark.parametrize("io", ["bf16", "fp32"])
+@pytest.mark.parametrize("shape,rate", [((1, 1100, 1, 2, 128, 128), (-8.0, -5.0)), ((2, 1601, 2, 2, 64, 32), (-9.0, 0.0)),
+                                        ((1, 2573, 1, 1, 32, 64), (-7.0, -4.0)), ((1, 1537, 1, 3, 128, 64), (-3.0, 2.0)),
+                                        ((1, 6 * 256, 2, 2, 64, 128), (-9.0, -5.0))], ids=str)
+def test_backward_split(shape, rate, io):
+    """Few long rows, whose walks are cut into segments; states and gradients carry far."""
+    d, opt = make(*shape, io, seed=shape[1] + 1, rate=rate)
+    check_backward(d, opt, io)
+    check_backward(dict(d, S0=None), opt, io, with_dS=False)
+
+
 def test_backward_empty():
     d, opt = make(2, 0, 1, 2, 32, 32, "bf16", raw=True)
     got = check_backward(d, opt, "bf16")
