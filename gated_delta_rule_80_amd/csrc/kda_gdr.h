@@ -73,13 +73,18 @@ struct GdrShape {
 // parallelism, so it pays from 6 segments on, while workgroups stay within the 256
 // CUs; segments of at least 4 chunks keep the composition (about 1 us a segment)
 // below the walks.  Measured at 64k tokens, 12 heads, D = 128, bf16 (the whole call):
-// 0.79 ms in 21 segments, 2.88 ms unsplit.
+// 0.79 ms in 21 segments, 2.88 ms unsplit.  The backward does more beside its walks (three
+// maps and two compositions) and fills the card with both of them sooner: it splits where
+// the CUs leave room for 8 segments (64k tokens, 12 heads: 2.22 against 4.65 ms; 32 heads,
+// 8 segments: 0.72 against 0.79 ms at 8192 tokens, 0.45 against 0.43 at 4096; 40 heads in 6
+// segments would take 0.39 against 0.33 ms at 3000).
 struct GdrSplit {
   int nseg, seg_len;
 };
-constexpr GdrSplit gdr_split(long walks, int nch, int Dv, bool fp32) {
+constexpr GdrSplit gdr_split(long walks, int nch, int Dv, bool fp32, bool bwd) {
   const long vb = Dv >= 128 && !fp32 ? 128 : (Dv >= 64 ? 64 : 32);
   long P = 256 / (walks * (Dv / vb) > 0 ? walks * (Dv / vb) : 1);
+  if (bwd && P < 8) return {1, nch};
   if (nch / 4 < P) P = nch / 4;
   if (P > 64) P = 64;
   if (P < 6) return {1, nch};

@@ -136,9 +136,9 @@ kda_status disjoint(const Spans& outs, const Spans& ins) {
 struct GdrWork {
   size_t seq, rec, y, ckS, ckdS, dg, starts, maps, ends, bytes;
 };
-GdrSplit split_of(const kda_gdr_args* a, const GdrSizes& s) {
+GdrSplit split_of(const kda_gdr_args* a, const GdrSizes& s, bool bwd) {
   if (gdr_packed(a) || a->T == 0) return {1, s.NT};
-  return gdr_split((long)a->B * a->Hv, s.NT, a->Dv, a->io == KDA_FP32);
+  return gdr_split((long)a->B * a->Hv, s.NT, a->Dv, a->io == KDA_FP32, bwd);
 }
 bool gdr_work(const kda_gdr_args* a, const GdrSizes& s, bool bwd, GdrWork& w) {
   const size_t es = esize(a->io);
@@ -159,7 +159,7 @@ bool gdr_work(const kda_gdr_args* a, const GdrSizes& s, bool bwd, GdrWork& w) {
   w.dg = round_up(w.ckdS + ck, 256);
   w.starts = w.maps = w.ends = round_up(w.dg + dg, 256);
   w.bytes = w.starts;
-  if (const GdrSplit sp = split_of(a, s); sp.nseg > 1) {
+  if (const GdrSplit sp = split_of(a, s, bwd); sp.nseg > 1) {
     // at most 256 workgroups of segments: these sizes stay small
     const size_t n = (size_t)a->B * a->Hv * sp.nseg * a->Dk * 4;
     w.maps = w.starts + n * a->Dv;
@@ -269,7 +269,7 @@ kda_status kda_gdr_prefill(const kda_gdr_args* a, void* ws, size_t ws_bytes, voi
   p.q = a->q; p.k = a->k; p.v = a->v;
   p.rec = base + w.rec;
   p.S0 = a->S0; p.S_T = a->S_T; p.o = a->o;
-  const GdrSplit sp = split_of(a, s);
+  const GdrSplit sp = split_of(a, s, false);
   p.nseg = sp.nseg;
   p.seg_len = sp.seg_len;
   p.starts = reinterpret_cast<float*>(base + w.starts);
@@ -347,7 +347,7 @@ kda_status kda_gdr_prefill_backward(const kda_gdr_backward_args* a, void* ws, si
   p.y = base + w.y;
   p.ckpt = base + w.ckS;
   p.bwd = 1;
-  const GdrSplit sp = split_of(f, s);
+  const GdrSplit sp = split_of(f, s, true);
   p.nseg = sp.nseg;
   p.seg_len = sp.seg_len;
   p.starts = reinterpret_cast<float*>(base + w.starts);
