@@ -92,6 +92,17 @@ constexpr GdrSplit gdr_split(long walks, int nch, int Dv, bool fp32, bool bwd) {
   return {(nch + len - 1) / len, len};
 }
 
+// Packed rows, whose lengths the host does not know: segments of a length that fills the
+// CUs once, where the mean sequence has at least 6 of them.  {most segments, length}.
+constexpr GdrSplit gdr_split_packed(long tokens, int C, long n_seqs, long Hv, int Dv, bool fp32) {
+  const long vb = Dv >= 128 && !fp32 ? 128 : (Dv >= 64 ? 64 : 32);
+  const long nch = (tokens + C - 1) / C;
+  long len = (nch * Hv * (Dv / vb) + 255) / 256;
+  if (len < 4) len = 4;
+  if (nch < 6 * len * n_seqs) return {1, (int)nch};
+  return {(int)(tokens / (C * len) + n_seqs), (int)len};
+}
+
 // Whether a walk's workgroup takes 128 value columns (8 waves) or 64 (4 waves) with
 // bf16 inputs; LDS holds one workgroup of either.  A chunk takes 5.2 and 3.3 us
 // (kda_gdr_walk.h): up to 128 walks the halves find a CU each and are the faster, more
@@ -150,7 +161,11 @@ struct GdrWalkParams {
   //   starts [B Hv][nseg][Dk][Dv] float32: at index s + 1 first the N of segment s,
   //          then the state at the start of segment s + 1; index 0: S0
   //   maps   [B Hv][nseg][Dk][Dk] float32: M of segments 1 .. nseg - 2
+  // Packed: each sequence has its own number of segments, segstart[b + 1] - segstart[b]
+  // (device; nseg bounds their total), and [B Hv][nseg] above is [Hv][nseg] with the
+  // sequences' segments behind one another.
   int nseg, seg_len;
+  const int* segstart;
   float* starts;
   float* maps;
   int pass;  // 0: outputs; 1: N; 2: M

@@ -134,10 +134,12 @@ kda_status disjoint(const Spans& outs, const Spans& ins) {
 // checkpoints per chunk and the float32 gradient of the decay, and of a split walk the
 // segments' starts, maps and (backward) ends.
 struct GdrWork {
-  size_t seq, rec, y, ckS, ckdS, dg, starts, maps, ends, bytes;
+  size_t seq, segs, rec, y, ckS, ckdS, dg, starts, maps, ends, bytes;
 };
 GdrSplit split_of(const kda_gdr_args* a, const GdrSizes& s, bool bwd) {
-  if (gdr_packed(a) || a->T == 0) return {1, s.NT};
+  if (a->T == 0 || (gdr_packed(a) && bwd)) return {1, s.NT};
+  if (gdr_packed(a))
+    return gdr_split_packed(a->T, gdr_chunk(a->io == KDA_FP32), a->n_seqs, a->Hv, a->Dv, a->io == KDA_FP32);
   return gdr_split((long)a->B * a->Hv, s.NT, a->Dv, a->io == KDA_FP32, bwd);
 }
 bool gdr_work(const kda_gdr_args* a, const GdrSizes& s, bool bwd, GdrWork& w) {
@@ -152,7 +154,9 @@ bool gdr_work(const kda_gdr_args* a, const GdrSizes& s, bool bwd, GdrWork& w) {
     dg = a->A_log != nullptr ? s.gates / es * 4 : 0;
   }
   w.seq = 0;
-  w.rec = round_up(gdr_packed(a) ? 8 * ((size_t)a->n_seqs + 1) : 0, 256);
+  // the tables of chunks, and of a split walk those of segments
+  w.segs = round_up(gdr_packed(a) ? 8 * ((size_t)a->n_seqs + 1) : 0, 256);
+  w.rec = w.segs + (gdr_packed(a) && split_of(a, s, bwd).nseg > 1 ? round_up(8 * ((size_t)a->n_seqs + 1), 256) : 0);
   w.y = w.rec + recs;
   w.ckS = round_up(w.y + y, 256);
   w.ckdS = round_up(w.ckS + ck, 256);
@@ -160,7 +164,7 @@ bool gdr_work(const kda_gdr_args* a, const GdrSizes& s, bool bwd, GdrWork& w) {
   w.starts = w.maps = w.ends = round_up(w.dg + dg, 256);
   w.bytes = w.starts;
   if (const GdrSplit sp = split_of(a, s, bwd); sp.nseg > 1) {
-    // at most 256 workgroups of segments: these sizes stay small
+    // about 256 workgroups of segments: these sizes stay small
     const size_t n = (size_t)a->B * a->Hv * sp.nseg * a->Dk * 4;
     w.maps = w.starts + n * a->Dv;
     w.ends = w.maps + n * a->Dk;
@@ -270,6 +274,17 @@ kda_status kda_gdr_prefill(const kda_gdr_args* a, void* ws, size_t ws_bytes, voi
   p.rec = base + w.rec;
   p.S0 = a->S0; p.S_T = a->S_T; p.o = a->o;
   const GdrSplit sp = split_of(a, s, false);
+  if (gdr_packed(a) && sp.nseg > 1) {
+    IndexParams ip{};
+    ip.cu_seqlens = a->cu_seqlens;
+    ip.bounds = reinterpret_cast<int*>(base + w.segs);
+    ip.cstart = ip.bounds + a->n_seqs + 1;
+    ip.n_seqs = a->n_seqs;
+    ip.T = a->T;
+    ip.C = gdr_chunk(a->io == KDA_FP32) * sp.seg_len;
+    p.segstart = ip.cstart;
+    if (kda_status e = hip_status(launch_seq_index(ip, st)); e != KDA_OK) return e;
+  }
   p.nseg = sp.nseg;
   p.seg_len = sp.seg_len;
   p.starts = reinterpret_cast<float*>(base + w.starts);

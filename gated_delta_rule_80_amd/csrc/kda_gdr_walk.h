@@ -62,13 +62,26 @@ __device__ __forceinline__ void gdr_walk(const GdrWalkParams& p, int Dv, int blk
   static_assert(RB.t == R.t && RB.sc == R.sc, "one place in both records");
   const size_t rec_bytes = !OUT && !CK && p.bwd ? RB.bytes : R.bytes;
   const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6), r = lane & 15, g4 = lane >> 4;
-  int bh, vblk, seg = 0;
+  int bh, vblk, seg = 0, nseg = p.nseg;
   if (!gdr_walk_id(blk, Dv / VB, p.s.Hv / p.s.Hk, p.walks, bh, vblk)) return;  // uniform
   bh += p.walk0;
+  size_t seg_idx = 0;  // of this segment in starts and maps
   if (p.nseg > 1) {
-    const int walks = p.s.B * p.s.Hv;
-    seg = bh / walks + (p.pass == 2 ? 1 : 0);  // the first segment needs no M
-    bh %= walks;
+    if (p.segstart == nullptr) {
+      const int walks = p.s.B * p.s.Hv;
+      seg = bh / walks + (p.pass == 2 ? 1 : 0);  // the first segment needs no M
+      bh %= walks;
+      seg_idx = (size_t)bh * nseg + seg;
+    } else {
+      const int id = bh / p.s.Hv, hh = bh % p.s.Hv;
+      if (id >= uniform(p.segstart[p.s.NS])) return;  // uniform
+      const int q = uniform(seq_of_slot(p.segstart, p.s.NS, id)), s0 = uniform(p.segstart[q]);
+      nseg = uniform(p.segstart[q + 1]) - s0;
+      seg = id - s0;
+      if (p.pass != 0 && (seg == nseg - 1 || (p.pass == 2 && seg == 0))) return;  // uniform: no map needed
+      seg_idx = (size_t)hh * p.nseg + id;
+      bh = q * p.s.Hv + hh;
+    }
   }
   const int h = bh % p.s.Hv, b = bh / p.s.Hv, hk = h / (p.s.Hv / p.s.Hk);
   GdrSpan sp = gdr_span(p.s, b, h, C);
@@ -127,12 +140,12 @@ __device__ __forceinline__ void gdr_walk(const GdrWalkParams& p, int Dv, int blk
   Terms<IO, 2> s2[NV][NUK];
   const size_t sbase = (size_t)bh * DK * Dv + v0 + r;
   // where this walk's state comes from (NULL: zeros) and goes to (NULL: nowhere)
-  const size_t seg_at = ((size_t)bh * p.nseg + seg) * DK * Dv + v0 + r;
+  const size_t seg_at = seg_idx * DK * Dv + v0 + r;
   const float* s_in = p.S0 != nullptr && seg == 0 ? p.S0 + sbase : nullptr;
   float* s_out = p.S_T != nullptr ? p.S_T + sbase : nullptr;
   if (p.nseg > 1) {
-    if (p.pass == 0) s_in = p.starts + seg_at;
-    if (p.pass == 0 && seg < p.nseg - 1) s_out = nullptr;
+    if (p.pass == 0 && nseg > 1) s_in = p.starts + seg_at;
+    if (p.pass == 0 && seg < nseg - 1) s_out = nullptr;
     if (p.pass == 1) s_out = p.starts + seg_at + (size_t)DK * Dv;
     if (p.pass == 2) s_out = p.maps + seg_at;
   }

@@ -22,8 +22,21 @@ __global__ __launch_bounds__(4 * DK) void kda_gdr_compose_kernel(GdrWalkParams p
   __shared__ __attribute__((aligned(16))) float st[2][16 * LS];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, r = lane & 15, g4 = lane >> 4;
   const int bh = blockIdx.x / (Dv / 16), v0 = blockIdx.x % (Dv / 16) * 16;
-  float* starts = p.starts + (size_t)bh * p.nseg * DK * Dv + v0;
-  const float* maps = p.maps + (size_t)bh * p.nseg * DK * DK;
+  int nseg = p.nseg;
+  size_t idx = (size_t)bh * nseg;
+  if (p.segstart != nullptr) {
+    const int b = bh / p.s.Hv, s0 = uniform(p.segstart[b]);
+    nseg = uniform(p.segstart[b + 1]) - s0;
+    idx = (size_t)(bh % p.s.Hv) * p.nseg + s0;
+    if (nseg == 0)  // a sequence without tokens has no segment to hand its state on
+      for (int i = tid; i < 16 * DK; i += 4 * DK) {
+        const size_t at = ((size_t)bh * DK + (i >> 4)) * Dv + v0 + (i & 15);
+        p.S_T[at] = p.S0 != nullptr ? p.S0[at] : 0.f;
+      }
+  }
+  if (nseg < 3) return;  // uniform: the second segment's start is there
+  float* starts = p.starts + idx * DK * Dv + v0;
+  const float* maps = p.maps + idx * DK * DK;
 
   auto terms = [](const float* x, bf16x8 (&t)[3]) {
     Terms<__bf16, 3> y;
@@ -38,9 +51,9 @@ __global__ __launch_bounds__(4 * DK) void kda_gdr_compose_kernel(GdrWalkParams p
     f32x4 n;
   };
   constexpr int D = REV ? -1 : 1;
-  const int first = REV ? p.nseg - 2 : 1;
+  const int first = REV ? nseg - 2 : 1;
   auto fetch = [&](int i, Rows& x) {  // of step i (past the last: of the last)
-    const int s = first + D * (i < p.nseg - 2 ? i : p.nseg - 3);
+    const int s = first + D * (i < nseg - 2 ? i : nseg - 3);
 #pragma unroll
     for (int u = 0; u < NU; ++u) {
       if constexpr (REV) {
@@ -76,9 +89,9 @@ __global__ __launch_bounds__(4 * DK) void kda_gdr_compose_kernel(GdrWalkParams p
   // the state the chain begins with, column by column
   for (int i = tid; i < 16 * DK; i += 4 * DK)
     st[first & 1][(i & 15) * LS + (i >> 4)] = starts[((size_t)first * DK + (i >> 4)) * Dv + (i & 15)];
-  const int steps = p.nseg - 2;
+  const int steps = nseg - 2;
   Rows x, y;  // of this step and the next, whose reads are under way meanwhile
-  if (steps > 0) fetch(0, x);
+  fetch(0, x);
   lds_barrier();
   for (int i = 0; i < steps; i += 2) {
     fetch(i + 1, y);
@@ -106,12 +119,15 @@ template <int DK, typename IO>
 static hipError_t launch_walk_d(const GdrWalkParams& all, int Dv, hipStream_t st) {
   GdrWalkParams p = all;
   p.walk0 = 0;
-  p.walks = p.s.NS * p.s.Hv * (p.nseg > 1 ? (p.pass == 0 ? p.nseg : p.nseg - p.pass) : 1);
+  const bool packed = p.s.seqs.bounds != nullptr;
+  const long most = (long)p.s.Hv * (p.nseg > 1 ? (packed ? p.nseg : (long)p.s.NS * p.nseg) : p.s.NS);
+  p.walks = (int)most;
+  if (p.nseg > 1 && !packed && p.pass != 0) p.walks = p.s.NS * p.s.Hv * (p.nseg - p.pass);
   if (Dv == 32) return launch_pass<DK, 2, 1, IO>(p, Dv, st);
   if constexpr (sizeof(IO) == 2)
-    if (gdr_whole_head((long)p.s.NS * p.s.Hv * (p.nseg > 1 ? p.nseg : 1), Dv)) {
+    if (gdr_whole_head(most, Dv)) {
       GdrWalkParams whole = p;
-      const int rest = p.nseg > 1 || p.s.seqs.bounds != nullptr ? 0 : gdr_last_walks(p.walks);
+      const int rest = p.nseg > 1 || packed ? 0 : gdr_last_walks(p.walks);
       whole.walks -= rest;
       if (hipError_t e = launch_pass<DK, 8, 1, IO>(whole, Dv, st); e != hipSuccess || rest == 0) return e;
       whole.walk0 = whole.walks;
@@ -136,7 +152,7 @@ static hipError_t walk(const GdrWalkParams& p, int Dk, int cols, bool fp32, hipS
 }
 
 template <bool REV> static hipError_t launch_compose(const GdrWalkParams& p, int Dk, int Dv, hipStream_t st) {
-  const dim3 grid((unsigned)((size_t)p.s.B * p.s.Hv * (Dv / 16)));
+  const dim3 grid((unsigned)((size_t)p.s.NS * p.s.Hv * (Dv / 16)));
   switch (Dk) {
     case 32: hipLaunchKernelGGL((kda_gdr_compose_kernel<32, REV>), grid, dim3(128), 0, st, p, Dv); break;
     case 64: hipLaunchKernelGGL((kda_gdr_compose_kernel<64, REV>), grid, dim3(256), 0, st, p, Dv); break;

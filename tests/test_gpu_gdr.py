@@ -167,6 +167,29 @@ def test_packed_many_sequences(io):
     check_backward(d, opt, io, cu)
 
 
+@pytest.mark.parametrize("io", ["bf16", "fp32"])
+@pytest.mark.parametrize("lens", [[0, 2000, 1, 0, 4100, 700, 257, 0], [3000], [0, 5000, 0], [900, 2600, 63, 1700]], ids=str)
+def test_packed_split(lens, io):
+    """Long prompts of few heads: each sequence's walk is cut into its own segments."""
+    T = sum(lens)
+    d, opt = make(1, T, 1, 2, 64, 64, io, n_seqs=len(lens), seed=T, rate=(-9.0, -5.0))
+    cu = torch.tensor([0] + list(np.cumsum(lens)), dtype=torch.int32)
+    o, S = check_forward(d, opt, io, cu)
+    x = d["S0"].cuda()  # the states in place
+    o2, _ = kda.kda_gdr_prefill(*[d[n].cuda() for n in ("q", "k", "v", "g", "beta")], x, S_T=x, cu_seqlens=cu.cuda())
+    assert torch.equal(o, o2) and torch.equal(S, x)
+    check_forward(dict(d, S0=None), opt, io, cu)
+    # offsets that leave a gap, or go down (read as their running maximum)
+    cu[0], cu[-1] = min(lens[0], 40), T - 3
+    o = torch.full((1, T, 2, 64), 7.0, dtype=DT[io], device="cuda")
+    _, S = forward(d, opt, cu, o=o)
+    at = np.maximum.accumulate(cu.numpy()).tolist()
+    ro, rS = ref.gdr_reference(*[num(d[n]) for n in ("q", "k", "v", "g", "beta", "S0")], cu_seqlens=at)
+    a, b = at[0], at[-1]
+    assert rel(o[:, a:b], ro[:, a:b]) <= OUT[io] and rel(S, rS) <= STATE[io]
+    assert (o[:, :a] == 7).all() and (o[:, b:] == 7).all()
+
+
 def test_prefill_no_tokens():
     d, opt = make(2, 0, 1, 2, 32, 64, "bf16")
     o, S = forward(d, opt)
