@@ -94,6 +94,8 @@ constexpr GdrSplit gdr_split(long walks, int nch, int Dv, bool fp32, bool bwd) {
 
 // Packed rows, whose lengths the host does not know: segments of a length that fills the
 // CUs once, where the mean sequence has at least 6 of them.  {most segments, length}.
+// Whole calls, bf16, D = 128, split and unsplit: 8000 tokens, 8 heads 174 and 363 us; four
+// prompts of 4096, 8 heads 183 and 213 us; 20000 tokens, 32 heads 650 and 990 us.
 constexpr GdrSplit gdr_split_packed(long tokens, int C, long n_seqs, long Hv, int Dv, bool fp32) {
   const long vb = Dv >= 128 && !fp32 ? 128 : (Dv >= 64 ? 64 : 32);
   const long nch = (tokens + C - 1) / C;
