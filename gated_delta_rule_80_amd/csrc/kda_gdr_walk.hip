@@ -3,10 +3,22 @@
 
 namespace kda {
 
-template <int DK, int WV, int NV, typename IO, bool OUT>
+template <int DK, int WV, int NV, typename IO>
 __global__ __launch_bounds__(64 * WV) void kda_gdr_walk_kernel(GdrWalkParams p, int Dv) {
-  __shared__ __attribute__((aligned(16))) char lds[2 * GdrWalkLds<DK, WV, NV, IO, OUT>::BYTES];
-  gdr_walk<DK, WV, NV, IO, OUT, false>(p, Dv, blockIdx.x, lds);
+  __shared__ __attribute__((aligned(16))) char lds[2 * GdrWalkLds<DK, WV, NV, IO, true>::BYTES];
+  gdr_walk<DK, WV, NV, IO, true, false>(p, Dv, blockIdx.x, lds);
+}
+
+// The maps of a split walk in one launch: its first `half` workgroups walk for N, the
+// others for M (1000 float32 tokens of 8 heads, where each is a few workgroups: 52 us a
+// call with a launch each, 42 so).
+template <int DK, int WV, int NV, typename IO>
+__global__ __launch_bounds__(64 * WV) void kda_gdr_maps_kernel(GdrWalkParams p, int Dv, int half, int walks_m) {
+  __shared__ __attribute__((aligned(16))) char lds[2 * GdrWalkLds<DK, WV, NV, IO, false>::BYTES];
+  const bool second = (int)blockIdx.x >= half;
+  p.pass = second ? 2 : 1;
+  if (second) p.walks = walks_m;
+  gdr_walk<DK, WV, NV, IO, false, false>(p, second ? DK : Dv, (int)blockIdx.x - (second ? half : 0), lds);
 }
 
 // Composes the segments' starts: start_{s+1} = M_s start_s + N_s, in place in
@@ -108,26 +120,62 @@ template <int DK, int WV, int NV, typename IO>
 static hipError_t launch_pass(const GdrWalkParams& p, int Dv, hipStream_t st) {
   const dim3 grid((unsigned)gdr_walk_grid(p.walks, p.s.Hv / p.s.Hk, Dv / (16 * NV * WV))), block(64 * WV);
   if (grid.x == 0) return hipSuccess;
-  if (p.pass != 0)
-    hipLaunchKernelGGL((kda_gdr_walk_kernel<DK, WV, NV, IO, false>), grid, block, 0, st, p, Dv);
-  else
-    hipLaunchKernelGGL((kda_gdr_walk_kernel<DK, WV, NV, IO, true>), grid, block, 0, st, p, Dv);
+  hipLaunchKernelGGL((kda_gdr_walk_kernel<DK, WV, NV, IO>), grid, block, 0, st, p, Dv);
   return hipGetLastError();
+}
+
+// the walks of a pass: all, or all segments that need the map
+static int pass_walks(const GdrWalkParams& p, int pass) {
+  if (p.nseg <= 1) return p.s.NS * p.s.Hv;
+  if (p.s.seqs.bounds != nullptr) return p.nseg * p.s.Hv;
+  return p.s.NS * p.s.Hv * (p.nseg - pass);
+}
+
+template <int DK, int WV, int NV, typename IO>
+static hipError_t launch_maps_t(const GdrWalkParams& p, int Dv, bool n, bool m, hipStream_t st) {
+  const int share = p.s.Hv / p.s.Hk, walks_m = pass_walks(p, 2);
+  const size_t half = n ? gdr_walk_grid(p.walks, share, Dv / (16 * NV * WV)) : 0;
+  const size_t rest = m ? gdr_walk_grid(walks_m, share, DK / (16 * NV * WV)) : 0;
+  hipLaunchKernelGGL((kda_gdr_maps_kernel<DK, WV, NV, IO>), dim3((unsigned)(half + rest)), dim3(64 * WV), 0, st, p, Dv,
+                     (int)half, walks_m);
+  return hipGetLastError();
+}
+
+// waves of a workgroup for `cols` value columns
+template <typename IO> static int map_waves(const GdrWalkParams& p, int cols) {
+  if (cols == 32) return 2;
+  return sizeof(IO) == 2 && gdr_whole_head(pass_walks(p, 0), cols) ? 8 : 4;
+}
+
+template <int DK, typename IO>
+static hipError_t launch_maps_d(const GdrWalkParams& all, int Dv, hipStream_t st) {
+  GdrWalkParams p = all;
+  p.walk0 = 0;
+  p.walks = pass_walks(p, 1);
+  const int wn = map_waves<IO>(p, Dv), wm = map_waves<IO>(p, DK);
+  // together, or each with its own shape
+  for (int wv : {2, 4, 8}) {
+    const bool n = wn == wv, m = wm == wv;
+    if (!n && !m) continue;
+    hipError_t e;
+    if (wv == 2) e = launch_maps_t<DK, 2, 1, IO>(p, Dv, n, m, st);
+    else if (wv == 4) e = launch_maps_t<DK, 4, 1, IO>(p, Dv, n, m, st);
+    else e = launch_maps_t<DK, sizeof(IO) == 2 ? 8 : 4, 1, IO>(p, Dv, n, m, st);
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
 }
 
 template <int DK, typename IO>
 static hipError_t launch_walk_d(const GdrWalkParams& all, int Dv, hipStream_t st) {
   GdrWalkParams p = all;
   p.walk0 = 0;
-  const bool packed = p.s.seqs.bounds != nullptr;
-  const long most = (long)p.s.Hv * (p.nseg > 1 ? (packed ? p.nseg : (long)p.s.NS * p.nseg) : p.s.NS);
-  p.walks = (int)most;
-  if (p.nseg > 1 && !packed && p.pass != 0) p.walks = p.s.NS * p.s.Hv * (p.nseg - p.pass);
+  p.walks = pass_walks(p, 0);
   if (Dv == 32) return launch_pass<DK, 2, 1, IO>(p, Dv, st);
   if constexpr (sizeof(IO) == 2)
-    if (gdr_whole_head(most, Dv)) {
+    if (gdr_whole_head(p.walks, Dv)) {
       GdrWalkParams whole = p;
-      const int rest = p.nseg > 1 || packed ? 0 : gdr_last_walks(p.walks);
+      const int rest = p.nseg > 1 || p.s.seqs.bounds != nullptr ? 0 : gdr_last_walks(p.walks);
       whole.walks -= rest;
       if (hipError_t e = launch_pass<DK, 8, 1, IO>(whole, Dv, st); e != hipSuccess || rest == 0) return e;
       whole.walk0 = whole.walks;
@@ -167,11 +215,13 @@ hipError_t launch_gdr_compose(const GdrWalkParams& p, int Dk, int Dv, bool rever
 
 // the segments' maps, and their starts from them
 hipError_t launch_gdr_maps(const GdrWalkParams& p, int Dk, int Dv, bool fp32, hipStream_t st) {
-  GdrWalkParams q = p;
-  q.pass = 1;
-  if (hipError_t e = walk(q, Dk, Dv, fp32, st); e != hipSuccess) return e;
-  q.pass = 2;
-  if (hipError_t e = walk(q, Dk, Dk, fp32, st); e != hipSuccess) return e;
+  hipError_t e = hipErrorInvalidValue;
+  switch (Dk) {
+    case 32: e = fp32 ? launch_maps_d<32, float>(p, Dv, st) : launch_maps_d<32, __bf16>(p, Dv, st); break;
+    case 64: e = fp32 ? launch_maps_d<64, float>(p, Dv, st) : launch_maps_d<64, __bf16>(p, Dv, st); break;
+    case 128: e = fp32 ? launch_maps_d<128, float>(p, Dv, st) : launch_maps_d<128, __bf16>(p, Dv, st); break;
+  }
+  if (e != hipSuccess) return e;
   return launch_gdr_compose(p, Dk, Dv, false, st);
 }
 
