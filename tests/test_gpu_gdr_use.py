@@ -106,6 +106,19 @@ def test_garbage_outside_sequences(io):
         assert not b[n][:, dirty].any(), n
 
 
+def test_garbage_outside_long_sequences():
+    d, opt = make(1, 3000, 1, 2, 64, 64, "bf16", n_seqs=3, raw=True)
+    cu = [37, 1500, 1500, 2900]
+    e = {n: x.clone() for n, x in d.items()}
+    for n in ("q", "k", "v", "g", "beta"):
+        e[n][:, :37] = e[n][:, 2900:] = float("nan")
+    d, e, opt = ({n: dev(x) for n, x in y.items()} for y in (d, e, opt))
+    o, o2 = torch.zeros_like(d["v"]), torch.zeros_like(d["v"])
+    S, S2 = call(d, opt, cu_seqlens=i32(cu), o=o)[1], call(e, opt, cu_seqlens=i32(cu), o=o2)[1]
+    assert torch.equal(o, o2) and torch.equal(S, S2) and torch.equal(S[1], d["S0"][1])
+    assert not o[:, :37].any() and not o[:, 2900:].any()
+
+
 def test_garbage_in_padding_rows_and_free_pages():
     d, _ = on_gpu(1, 8, 2, 4, 64, 64, io="bf16")
     x, S, slots = decode_case(d, 8, [2, -1, 0, 7, 2, 1 << 30, -(1 << 31), 1], 4)
@@ -198,6 +211,36 @@ def test_captured_and_replayed():
         torch.cuda.synchronize()
         for i, (x, y) in enumerate(zip(got, want)):
             assert torch.equal(x, y), (seed, i)
+
+
+def test_split_walks_captured_and_replayed():
+    """Long rows of few heads, equal and packed: the segments' tables, maps and starts are
+    made anew by every replay."""
+    d, opt = on_gpu(1, 3000, 1, 2, 64, 64, io="bf16", raw=True)
+    e, _ = on_gpu(1, 3000, 1, 2, 64, 64, io="bf16", raw=True, n_seqs=2)
+    cu = i32([0, 1400, 3000])
+
+    def run():
+        o, S = call(d, opt)
+        o2, S2 = call({**d, "S0": e["S0"]}, opt, cu_seqlens=cu)
+        return [o, S, o2, S2, *grads(d, opt).values()]
+
+    run()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        kept = run()
+    for seed, at in enumerate([10, 1700, 2999]):
+        x, _ = on_gpu(1, 3000, 1, 2, 64, 64, io="bf16", raw=True, seed=20 + seed)
+        for m in d:
+            d[m].copy_(x[m])
+        cu.copy_(i32([0, at, 3000]))
+        graph.replay()
+        got = [y.clone() for y in kept]
+        want = run()
+        torch.cuda.synchronize()
+        for i, (y, w) in enumerate(zip(got, want)):
+            assert torch.equal(y, w), (seed, i)
 
 
 def test_two_graphs_with_their_own_workspaces():
